@@ -4,10 +4,12 @@
  * The memory-bound ops that sit between the grouped GEMMs of a
  * Mixture-of-Experts layer and the residual stream (the seven of the hot path,
  * their dtype variants, the bounded SwiGLU, the fused epilogue chain and the
- * rank-order reduce-scatter), plus the IPC helpers under the reduce-scatter.
+ * rank-order reduce-scatter), plus the IPC helpers under the reduce-scatter;
+ * and the ops of the same block ahead of them: the layer norm and the top-k
+ * router, forward and backward.
  * Each op entry point takes caller-owned DEVICE pointers, sizes and a CUDA
- * stream, validates its arguments on the host, enqueues exactly one kernel on
- * `stream` and returns.
+ * stream, validates its arguments on the host, enqueues one kernel (where its
+ * comment says so, two or three) on `stream` and returns.
  *
  * Common contract
  *   - Ownership: every pointer is owned by the caller and must stay valid
@@ -82,6 +84,11 @@ typedef enum {
   MOE_ACT_SWIGLU = 2        /* silu(gate) * up, gate = first half of the row     */
 } moe_act;
 
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,    /* e^l over the sum of e^l                           */
+  MOE_SCORE_SIGMOID = 1     /* 1 / (1 + e^-l), each expert by itself             */
+} moe_score;
+
 enum {
   MOE_OK = 0,
   MOE_ERR_NULL = 1,  /* a required pointer is NULL                              */
@@ -89,14 +96,16 @@ enum {
                         size beyond the documented maximum                     */
   MOE_ERR_DTYPE = 3, /* dtype (or activation) not supported for that argument   */
   MOE_ERR_ALIGN = 4, /* a pointer not aligned to its element size               */
-  MOE_ERR_LIMIT = 5, /* limit or clamp_scale not a positive number              */
+  MOE_ERR_LIMIT = 5, /* limit or clamp_scale not a positive number; eps negative
+                        or not finite; scale not finite                         */
   MOE_ERR_CUDA = 6   /* a CUDA runtime call or the launch failed                */
 };
 
 /* Bits ORed into the optional device error word. */
 enum {
   MOE_DEVERR_COUNT = 1,  /* *n_used / *valid_tokens outside [0, max]: clamped    */
-  MOE_DEVERR_MAP = 2,    /* permutation_map entry >= num_probs: row skipped       */
+  MOE_DEVERR_MAP = 2,    /* permutation_map entry >= num_probs: row skipped; a
+                            chosen expert >= num_experts: its gradient skipped    */
   MOE_DEVERR_INVERSE = 4, /* inverse_map entry >= max_rows: contribution skipped  */
   MOE_DEVERR_TIMEOUT = 8  /* a kernel's barrier wait gave up (~1 s: a shared-memory
                              copy or a consumer that never completed).  The rows the
@@ -432,6 +441,93 @@ MOE_API int moe_unpermute_reduce_scatter(const void* const* expert_outputs, moe_
                                          const int32_t* rank_token_offset, moe_dtype partial_dt,
                                          void* out, moe_dtype out_dt, int64_t local_tokens,
                                          int64_t hidden, int32_t* dev_err, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm over the hidden axis, forward (the norm ahead of the router and
+ * the experts of a pre-norm block).
+ *   mean[r] = 1/hidden sum_h x[r, h]
+ *   rstd[r] = (1/hidden sum_h (x[r, h] - mean[r])^2 + eps)^-1/2
+ *   y[r, h] = (x[r, h] - mean[r]) * rstd[r] * weight[h] + bias[h]
+ * fp32 sums; one rounding to dt.
+ * x       dt [rows, ld_x], ld_x >= hidden
+ * weight  w_dt [hidden];  bias w_dt [hidden] or NULL (none); w_dt is dt or MOE_FP32
+ * y       dt [rows, ld_y], ld_y >= hidden; columns >= hidden are not written
+ * mean, rstd  fp32 [rows] (outputs for the backward), each may be NULL
+ * eps     finite, >= 0 (MOE_ERR_LIMIT otherwise)
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_layer_norm_fwd(const void* x, const void* weight, const void* bias, void* y,
+                               float* mean, float* rstd, int64_t rows, int64_t hidden,
+                               int64_t ld_x, int64_t ld_y, float eps, moe_dtype dt,
+                               moe_dtype w_dt, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm, backward, with the parameters' gradients.
+ *   xhat = (x - mean) * rstd,  a = grad_y * weight
+ *   grad_x[r, h]   = rstd * (a - 1/hidden sum_h a - xhat * 1/hidden sum_h a * xhat)
+ *   grad_weight[h] = sum_r grad_y * xhat,   grad_bias[h] = sum_r grad_y
+ * fp32 sums, one rounding to dt / w_dt.  The sums over the rows run in a fixed
+ * order that depends on rows, hidden and the alignment of the data alone; over
+ * no rows they are +0.  Enqueues two kernels (three for rows of more than 8192
+ * columns): the rows, then the partial sums of the row groups.
+ * mean, rstd   fp32 [rows], from the forward
+ * grad_bias    w_dt [hidden] or NULL (no bias)
+ * workspace    at least moe_layer_norm_bwd_workspace() bytes, 16-byte aligned
+ *              (MOE_ERR_SHAPE if workspace_bytes is less), contents irrelevant
+ *              before and after; one call at a time may use it
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_layer_norm_bwd_workspace(int64_t rows, int64_t hidden, int64_t* bytes);
+MOE_API int moe_layer_norm_bwd(const void* grad_y, const void* x, const void* weight,
+                               const float* mean, const float* rstd, void* grad_x,
+                               void* grad_weight, void* grad_bias, void* workspace,
+                               int64_t workspace_bytes, int64_t rows, int64_t hidden,
+                               int64_t ld_gy, int64_t ld_x, int64_t ld_gx, moe_dtype dt,
+                               moe_dtype w_dt, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Router: the top_k experts of each token and their routing weights.
+ *   ids[t, k]     = expert of token t's k-th largest logit (ties: the lower
+ *                   expert first; NaN counts as the largest; -inf is never
+ *                   chosen: a slot that finds nothing else gets id -1)
+ *   weights[t, k] = scale * score, 0 for id -1, where score is
+ *     MOE_SCORE_SOFTMAX  e^l / sum over all experts; normalise: over the chosen
+ *     MOE_SCORE_SIGMOID  sig(l);  normalise: sig(l) / sum of the chosen sig
+ *   in fp32.  The weights, flat, are the `probs` of the other entry points
+ *   (index t * top_k + k).
+ * logits        dt [tokens, ld_logits], ld_logits >= num_experts
+ * weights, ids  fp32 / int32 [tokens, top_k] contiguous (outputs)
+ * valid_tokens  optional int32 (device): tokens >= *valid_tokens are neither
+ *               read nor written (MOE_DEVERR_COUNT if outside [0, tokens])
+ * num_experts   1 .. 1024;  top_k 1 .. min(32, num_experts)
+ * scale         finite (MOE_ERR_LIMIT otherwise)
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_router_topk_fwd(const void* logits, moe_dtype dt, float* weights, int32_t* ids,
+                                const int32_t* valid_tokens, int64_t tokens,
+                                int32_t num_experts, int32_t top_k, int64_t ld_logits,
+                                moe_score score, int normalise, float scale, int32_t* dev_err,
+                                cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Router, backward: the gradient of the logits from that of the weights (the
+ * choice itself has none).  With v = weights / scale, g = scale * grad_weights:
+ *   softmax              grad_j = v_j * ((j chosen) g_j - sum_chosen g v), every j
+ *   softmax, normalised  grad_i = v_i * (g_i - sum_chosen g v), 0 if not chosen
+ *   sigmoid              grad_i = g_i * sig(l_i) * (1 - sig(l_i)), 0 if not chosen
+ *   sigmoid, normalised  grad_i = v_i * (g_i - sum_chosen g v) * (1 - sig(l_i)),
+ *                        0 if not chosen
+ * ids           int32 [tokens, top_k]; < 0: no expert (its grad_weights is not
+ *               read); >= num_experts: skipped, MOE_DEVERR_MAP; an expert named
+ *               twice gets the sum of both gradients
+ * grad_weights  fp32 [tokens, top_k]
+ * grad_logits   dt [tokens, ld_grad], ld_grad >= num_experts (output; every
+ *               column < num_experts of the live tokens is written)
+ * valid_tokens, dev_err as for the forward
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t* ids,
+                                const float* grad_weights, void* grad_logits,
+                                const int32_t* valid_tokens, int64_t tokens,
+                                int32_t num_experts, int32_t top_k, int64_t ld_logits,
+                                int64_t ld_grad, moe_score score, int normalise, float scale,
+                                int32_t* dev_err, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Test hook of the failure path of the bounded waits (no counterpart on the

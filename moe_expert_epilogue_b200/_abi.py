@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_epilogue.so")
 
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_ACT_SQRELU, MOE_ACT_SQRELU_CLAMP, MOE_ACT_SWIGLU = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 (MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_LIMIT,
  MOE_ERR_CUDA) = range(7)
 MOE_DEVERR_COUNT, MOE_DEVERR_MAP, MOE_DEVERR_INVERSE, MOE_DEVERR_TIMEOUT = 1, 2, 4, 8
@@ -44,6 +45,13 @@ SIGNATURES = {
                                      _P, _P],
     "moe_unpermute_reduce_scatter": [_P, _I, _I64, _P, _I32, _I64, _P, _I32, _I32, _P, _I, _P,
                                      _I, _I64, _I64, _P, _P],
+    "moe_layer_norm_fwd": [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _F, _I, _I, _P],
+    "moe_layer_norm_bwd_workspace": [_I64, _I64, ctypes.POINTER(_I64)],
+    "moe_layer_norm_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                           _I, _I, _P],
+    "moe_router_topk_fwd": [_P, _I, _P, _P, _P, _I64, _I32, _I32, _I64, _I, _I, _F, _P, _P],
+    "moe_router_topk_bwd": [_P, _I, _P, _P, _P, _P, _I64, _I32, _I32, _I64, _I64, _I, _I, _F, _P,
+                            _P],
     "moe_symm_alloc": [ctypes.c_size_t, ctypes.POINTER(_P)],
     "moe_symm_free": [_P],
     "moe_ipc_export": [_P, ctypes.c_char_p],
@@ -216,6 +224,41 @@ def moe_unpermute_reduce_scatter(expert_outputs, eo_dt, max_rows, inverse_maps,
     _call("moe_unpermute_reduce_scatter", ptr(expert_outputs), eo_dt, max_rows, ptr(inverse_maps),
           num_local_experts, capacity_rows, ptr(ep_tokens), world, rank, ptr(rank_token_offset),
           partial_dt, ptr(out), out_dt, local_tokens, hidden, ptr(dev_err), stream_handle(stream))
+
+
+def moe_layer_norm_fwd(x, weight, bias, y, mean, rstd, rows, hidden, ld_x, ld_y, eps, dt, w_dt,
+                       stream=None):
+    _call("moe_layer_norm_fwd", ptr(x), ptr(weight), ptr(bias), ptr(y), ptr(mean), ptr(rstd), rows,
+          hidden, ld_x, ld_y, float(eps), dt, w_dt, stream_handle(stream))
+
+
+def moe_layer_norm_bwd_workspace(rows, hidden) -> int:
+    """Bytes of workspace that moe_layer_norm_bwd needs."""
+    v = _I64(0)
+    _call("moe_layer_norm_bwd_workspace", rows, hidden, ctypes.byref(v))
+    return int(v.value)
+
+
+def moe_layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias, workspace,
+                       workspace_bytes, rows, hidden, ld_gy, ld_x, ld_gx, dt, w_dt, stream=None):
+    _call("moe_layer_norm_bwd", ptr(grad_y), ptr(x), ptr(weight), ptr(mean), ptr(rstd), ptr(grad_x),
+          ptr(grad_weight), ptr(grad_bias), ptr(workspace), workspace_bytes, rows, hidden, ld_gy,
+          ld_x, ld_gx, dt, w_dt, stream_handle(stream))
+
+
+def moe_router_topk_fwd(logits, dt, weights, ids, valid_tokens, tokens, num_experts, top_k,
+                        ld_logits, score, normalise, scale, dev_err=None, stream=None):
+    _call("moe_router_topk_fwd", ptr(logits), dt, ptr(weights), ptr(ids), ptr(valid_tokens), tokens,
+          num_experts, top_k, ld_logits, score, int(bool(normalise)), float(scale), ptr(dev_err),
+          stream_handle(stream))
+
+
+def moe_router_topk_bwd(logits, dt, ids, grad_weights, grad_logits, valid_tokens, tokens,
+                        num_experts, top_k, ld_logits, ld_grad, score, normalise, scale,
+                        dev_err=None, stream=None):
+    _call("moe_router_topk_bwd", ptr(logits), dt, ptr(ids), ptr(grad_weights), ptr(grad_logits),
+          ptr(valid_tokens), tokens, num_experts, top_k, ld_logits, ld_grad, score,
+          int(bool(normalise)), float(scale), ptr(dev_err), stream_handle(stream))
 
 
 def moe_symm_alloc(nbytes: int) -> int:

@@ -144,6 +144,13 @@ inline bool aligned_to(const void* p, int64_t n) {
 // rows * cols fits comfortably in int64 element offsets
 inline bool product_ok(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / 8 / a; }
 inline bool limit_ok(float L) { return !std::isnan(L) && L > 0.0f; }
+inline bool eps_ok(float eps) { return std::isfinite(eps) && eps >= 0.0f; }
+inline bool score_ok(moe_score s) { return s == MOE_SCORE_SOFTMAX || s == MOE_SCORE_SIGMOID; }
+// One warp holds a token's logits and its choices, one a lane.
+inline bool router_shape_ok(int64_t tokens, int32_t experts, int32_t top_k) {
+  return tokens >= 0 && experts >= 1 && experts <= 1024 && top_k >= 1 && top_k <= 32 &&
+         top_k <= experts && product_ok(tokens, experts);
+}
 
 }  // namespace
 
@@ -425,6 +432,101 @@ int moe_unpermute_reduce_scatter(const void* const* expert_outputs, moe_dtype eo
       expert_outputs, eo_dt, max_rows, reinterpret_cast<const void* const*>(inverse_maps),
       num_local_experts, capacity_rows, ep_tokens, world, rank, rank_token_offset, partial_dt,
       out, out_dt, local_tokens, hidden, dev_err, stream);
+}
+
+int moe_layer_norm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean,
+                       float* rstd, int64_t rows, int64_t hidden, int64_t ld_x, int64_t ld_y,
+                       float eps, moe_dtype dt, moe_dtype w_dt, cudaStream_t stream) {
+  if (!dtype_ok(dt) || (w_dt != dt && w_dt != MOE_FP32)) return MOE_ERR_DTYPE;
+  if (rows < 0 || hidden < 0 || ld_x < hidden || ld_y < hidden || !product_ok(rows, ld_x) ||
+      !product_ok(rows, ld_y))
+    return MOE_ERR_SHAPE;
+  if (!eps_ok(eps)) return MOE_ERR_LIMIT;
+  if (rows == 0 || hidden == 0) return MOE_OK;
+  if (!x || !weight || !y) return MOE_ERR_NULL;
+  const int64_t es = dtype_size(dt), ws = dtype_size(w_dt);
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, ws) ||
+      !aligned_to(bias, ws) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return MOE_ERR_ALIGN;
+  return launch_layer_norm_fwd(x, weight, bias, y, mean, rstd, rows, hidden, ld_x, ld_y, eps, dt,
+                               w_dt, stream);
+}
+
+int moe_layer_norm_bwd_workspace(int64_t rows, int64_t hidden, int64_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  if (rows < 0 || hidden < 0 || !product_ok(2 * 4 * 148, hidden)) return MOE_ERR_SHAPE;
+  *bytes = layer_norm_bwd_workspace(rows, hidden);
+  return MOE_OK;
+}
+
+int moe_layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const float* mean,
+                       const float* rstd, void* grad_x, void* grad_weight, void* grad_bias,
+                       void* workspace, int64_t workspace_bytes, int64_t rows, int64_t hidden,
+                       int64_t ld_gy, int64_t ld_x, int64_t ld_gx, moe_dtype dt, moe_dtype w_dt,
+                       cudaStream_t stream) {
+  if (!dtype_ok(dt) || (w_dt != dt && w_dt != MOE_FP32)) return MOE_ERR_DTYPE;
+  if (rows < 0 || hidden < 0 || ld_gy < hidden || ld_x < hidden || ld_gx < hidden ||
+      !product_ok(rows, ld_gy) || !product_ok(rows, ld_x) || !product_ok(rows, ld_gx) ||
+      !product_ok(2 * 4 * 148, hidden))
+    return MOE_ERR_SHAPE;
+  if (hidden == 0) return MOE_OK;
+  if (!grad_weight) return MOE_ERR_NULL;
+  const int64_t es = dtype_size(dt), ws = dtype_size(w_dt);
+  if (!aligned_to(grad_weight, ws) || !aligned_to(grad_bias, ws)) return MOE_ERR_ALIGN;
+  if (rows == 0) {                                                   // empty sums: +0
+    if (int rc = zero_fill(grad_weight, hidden * ws, stream)) return rc;
+    return zero_fill(grad_bias, hidden * ws, stream);
+  }
+  if (!grad_y || !x || !weight || !mean || !rstd || !grad_x || !workspace) return MOE_ERR_NULL;
+  if (workspace_bytes < layer_norm_bwd_workspace(rows, hidden)) return MOE_ERR_SHAPE;
+  if (!aligned_to(grad_y, es) || !aligned_to(x, es) || !aligned_to(grad_x, es) ||
+      !aligned_to(weight, ws) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
+      !aligned_to(workspace, 16))
+    return MOE_ERR_ALIGN;
+  return launch_layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
+                               static_cast<float*>(workspace), rows, hidden, ld_gy, ld_x, ld_gx,
+                               dt, w_dt, stream);
+}
+
+int moe_router_topk_fwd(const void* logits, moe_dtype dt, float* weights, int32_t* ids,
+                        const int32_t* valid_tokens, int64_t tokens, int32_t num_experts,
+                        int32_t top_k, int64_t ld_logits, moe_score score, int normalise,
+                        float scale, int32_t* dev_err, cudaStream_t stream) {
+  if (!dtype_ok(dt) || !score_ok(score)) return MOE_ERR_DTYPE;
+  if (!router_shape_ok(tokens, num_experts, top_k) || ld_logits < num_experts ||
+      !product_ok(tokens, ld_logits))
+    return MOE_ERR_SHAPE;
+  if (!std::isfinite(scale)) return MOE_ERR_LIMIT;
+  if (tokens == 0) return MOE_OK;
+  if (!logits || !weights || !ids) return MOE_ERR_NULL;
+  if (!aligned_to(logits, dtype_size(dt)) || !aligned_to(weights, 4) || !aligned_to(ids, 4) ||
+      !aligned_to(valid_tokens, 4) || !aligned_to(dev_err, 4))
+    return MOE_ERR_ALIGN;
+  return launch_router_topk_fwd(logits, dt, weights, ids, valid_tokens, tokens, num_experts,
+                                top_k, ld_logits, score == MOE_SCORE_SOFTMAX, normalise != 0,
+                                scale, dev_err, stream);
+}
+
+int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t* ids,
+                        const float* grad_weights, void* grad_logits,
+                        const int32_t* valid_tokens, int64_t tokens, int32_t num_experts,
+                        int32_t top_k, int64_t ld_logits, int64_t ld_grad, moe_score score,
+                        int normalise, float scale, int32_t* dev_err, cudaStream_t stream) {
+  if (!dtype_ok(dt) || !score_ok(score)) return MOE_ERR_DTYPE;
+  if (!router_shape_ok(tokens, num_experts, top_k) || ld_logits < num_experts ||
+      ld_grad < num_experts || !product_ok(tokens, ld_logits) || !product_ok(tokens, ld_grad))
+    return MOE_ERR_SHAPE;
+  if (!std::isfinite(scale)) return MOE_ERR_LIMIT;
+  if (tokens == 0) return MOE_OK;
+  if (!logits || !ids || !grad_weights || !grad_logits) return MOE_ERR_NULL;
+  if (!aligned_to(logits, dtype_size(dt)) || !aligned_to(grad_logits, dtype_size(dt)) ||
+      !aligned_to(grad_weights, 4) || !aligned_to(ids, 4) || !aligned_to(valid_tokens, 4) ||
+      !aligned_to(dev_err, 4))
+    return MOE_ERR_ALIGN;
+  return launch_router_topk_bwd(logits, dt, ids, grad_weights, grad_logits, valid_tokens, tokens,
+                                num_experts, top_k, ld_logits, ld_grad,
+                                score == MOE_SCORE_SOFTMAX, normalise != 0, scale, dev_err,
+                                stream);
 }
 
 }  // extern "C"

@@ -25,10 +25,10 @@ int check_launch();
 // stream serialisation allowed (see pdl_prologue); a failure is left in the
 // runtime's error state for check_launch().
 template <typename... KArgs, typename... Args>
-inline void launch_kernel_block(void (*kernel)(KArgs...), int grid, int block, size_t smem,
-                                cudaStream_t stream, Args... args) {
+inline void launch_kernel_grid(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
+                               cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -38,6 +38,12 @@ inline void launch_kernel_block(void (*kernel)(KArgs...), int grid, int block, s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   (void)cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+inline void launch_kernel_block(void (*kernel)(KArgs...), int grid, int block, size_t smem,
+                                cudaStream_t stream, Args... args) {
+  launch_kernel_grid(kernel, dim3((unsigned)grid), block, smem, stream, args...);
 }
 
 template <typename... KArgs, typename... Args>
@@ -117,5 +123,22 @@ int launch_epilogue_fused(const void* expert_output, const float* row_probs, int
                           moe_dtype dt, int32_t* dev_err, cudaStream_t stream);
 int launch_residual_add(const void* e, const void* s, const void* r, void* out, int64_t numel,
                         moe_dtype dt, cudaStream_t stream);
+// fp32 bytes of the row groups' partial parameter gradients.
+int64_t layer_norm_bwd_workspace(int64_t rows, int64_t hidden);
+int launch_layer_norm_fwd(const void* x, const void* w, const void* b, void* y, float* mean,
+                          float* rstd, int64_t rows, int64_t hidden, int64_t ld_x, int64_t ld_y,
+                          float eps, moe_dtype dt, moe_dtype w_dt, cudaStream_t stream);
+int launch_layer_norm_bwd(const void* gy, const void* x, const void* w, const float* mean,
+                          const float* rstd, void* gx, void* gw, void* gb, float* ws,
+                          int64_t rows, int64_t hidden, int64_t ld_gy, int64_t ld_x,
+                          int64_t ld_gx, moe_dtype dt, moe_dtype w_dt, cudaStream_t stream);
+int launch_router_topk_fwd(const void* logits, moe_dtype dt, float* weights, int32_t* ids,
+                           const int32_t* valid, int64_t tokens, int E, int K, int64_t ld,
+                           bool softmax, bool normalise, float scale, int32_t* err,
+                           cudaStream_t stream);
+int launch_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t* ids, const float* gw,
+                           void* gl, const int32_t* valid, int64_t tokens, int E, int K,
+                           int64_t ld, int64_t ld_g, bool softmax, bool normalise, float scale,
+                           int32_t* err, cudaStream_t stream);
 
 }  // namespace moe

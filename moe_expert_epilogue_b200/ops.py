@@ -4,11 +4,13 @@ element of every output is produced by a kernel of libmoe_epilogue.so.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _abi
 from ._abi import (MOE_ACT_SQRELU, MOE_ACT_SQRELU_CLAMP, MOE_ACT_SWIGLU,  # noqa: F401
-                   MOE_BF16, MOE_FP16, MOE_FP32)
+                   MOE_BF16, MOE_FP16, MOE_FP32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX)
 
 _DT = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 
@@ -331,3 +333,144 @@ def unpermute_reduce_scatter(expert_outputs, eo_dtype, max_rows, inverse_maps, n
                                       moe_dtype(partial_dtype or eo_dtype), out,
                                       moe_dtype(out.dtype), out.shape[0], hidden, dev_err, stream)
     return out
+
+
+@contextlib.contextmanager
+def _other_place(device, stream):
+    with contextlib.ExitStack() as stack:
+        if device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            stack.enter_context(torch.cuda.stream(stream))
+        yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _ld(t, name):
+    """Leading dimension; of a single row whatever its stride says."""
+    return max(_rows_stride(t, name), t.shape[1])
+
+
+def _place(device, stream):
+    """Makes `device` (the tensors') and `stream` (None: the device's current one)
+    current, so that a call launches there and what it allocates belongs there."""
+    if not (device.type == "cuda" and torch.cuda.is_available()) or \
+            (stream is None and device.index == torch.cuda.current_device()):
+        return _HERE
+    return _other_place(device, stream)
+
+
+def layer_norm_fwd(x, weight, bias=None, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm of each row: y = (x - mean) * rstd * weight + bias, in x's dtype.
+    weight and bias (optional) have x's dtype or fp32.  Returns (y, mean, rstd), the
+    statistics fp32 [rows], for layer_norm_bwd."""
+    rows, hidden = _two_d(x, "x")
+    _check(x, "x", dtype=_FLOATS, contiguous=False)
+    _check(weight, "weight", dtype=(x.dtype, torch.float32), numel=hidden)
+    _check(bias, "bias", dtype=weight.dtype, numel=hidden)
+    with _place(x.device, stream):
+        if out is None:
+            out = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+        if mean is None:
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        _check(out, "out", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
+        _check(mean, "mean", dtype=torch.float32, numel=rows)
+        _check(rstd, "rstd", dtype=torch.float32, numel=rows)
+        ld_x, ld_y = _ld(x, "x"), _ld(out, "out")
+        _cuda(x, weight, bias, out, mean, rstd)
+        _abi.moe_layer_norm_fwd(x, weight, bias, out, mean, rstd, rows, hidden, ld_x, ld_y, eps,
+                                moe_dtype(x.dtype), moe_dtype(weight.dtype))
+    return out, mean, rstd
+
+
+def layer_norm_bwd(grad_y, x, weight, mean, rstd, has_bias=True, grad_x=None, grad_weight=None,
+                   grad_bias=None, workspace=None, stream=None):
+    """Returns (grad_x in x's dtype, grad_weight, grad_bias in weight's dtype; grad_bias
+    None if neither has_bias nor given).  mean and rstd are layer_norm_fwd's.  workspace (uint8, at least
+    layer_norm_bwd_workspace(rows, hidden) bytes) is allocated unless given."""
+    rows, hidden = _two_d(x, "x")
+    _check(x, "x", dtype=_FLOATS, contiguous=False)
+    _check(grad_y, "grad_y", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
+    _check(weight, "weight", dtype=(x.dtype, torch.float32), numel=hidden)
+    _check(mean, "mean", dtype=torch.float32, numel=rows)
+    _check(rstd, "rstd", dtype=torch.float32, numel=rows)
+    with _place(x.device, stream):
+        if grad_x is None:
+            grad_x = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+        if grad_weight is None:
+            grad_weight = torch.empty(hidden, dtype=weight.dtype, device=x.device)
+        if grad_bias is None and has_bias:
+            grad_bias = torch.empty(hidden, dtype=weight.dtype, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(layer_norm_bwd_workspace(rows, hidden), dtype=torch.uint8,
+                                    device=x.device)
+        _check(grad_x, "grad_x", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
+        _check(grad_weight, "grad_weight", dtype=weight.dtype, numel=hidden)
+        _check(grad_bias, "grad_bias", dtype=weight.dtype, numel=hidden)
+        _check(workspace, "workspace", dtype=torch.uint8)
+        ld_gy, ld_x, ld_gx = _ld(grad_y, "grad_y"), _ld(x, "x"), _ld(grad_x, "grad_x")
+        _cuda(grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias, workspace)
+        _abi.moe_layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
+                                workspace, workspace.numel(), rows, hidden, ld_gy, ld_x, ld_gx,
+                                moe_dtype(x.dtype), moe_dtype(weight.dtype))
+    return grad_x, grad_weight, grad_bias
+
+
+def layer_norm_bwd_workspace(rows, hidden) -> int:
+    """Bytes of workspace of layer_norm_bwd."""
+    return _abi.moe_layer_norm_bwd_workspace(rows, hidden)
+
+
+def router_topk_fwd(logits, top_k, score=MOE_SCORE_SOFTMAX, normalise=True, scale=1.0,
+                    weights=None, ids=None, valid_tokens=None, dev_err=None, stream=None):
+    """The top_k experts of each token: returns (weights fp32, ids int32), both
+    [tokens, top_k], by descending logit (ties: the lower expert first; -inf is never
+    chosen: id -1, weight 0).  score is MOE_SCORE_SOFTMAX (over all experts) or
+    MOE_SCORE_SIGMOID; normalise divides by the chosen experts' sum; scale multiplies.
+    Tokens at or past valid_tokens (int32 [1] on the device) are not written."""
+    tokens, experts = _two_d(logits, "logits")
+    _check(logits, "logits", dtype=_FLOATS, contiguous=False)
+    _check(valid_tokens, "valid_tokens", dtype=torch.int32, numel=1)
+    _check(dev_err, "dev_err", dtype=torch.int32, numel=1)
+    with _place(logits.device, stream):
+        if weights is None:
+            weights = torch.empty(tokens, top_k, dtype=torch.float32, device=logits.device)
+        if ids is None:
+            ids = torch.empty(tokens, top_k, dtype=torch.int32, device=logits.device)
+        _check(weights, "weights", dtype=torch.float32, shape=(tokens, top_k))
+        _check(ids, "ids", dtype=torch.int32, shape=(tokens, top_k))
+        ld = _ld(logits, "logits")
+        _cuda(logits, weights, ids, valid_tokens, dev_err)
+        _abi.moe_router_topk_fwd(logits, moe_dtype(logits.dtype), weights, ids, valid_tokens,
+                                 tokens, experts, top_k, ld, score, normalise, scale, dev_err)
+    return weights, ids
+
+
+def router_topk_bwd(logits, ids, grad_weights, score=MOE_SCORE_SOFTMAX, normalise=True,
+                    scale=1.0, grad_logits=None, valid_tokens=None, dev_err=None, stream=None):
+    """grad_logits (logits' dtype) from the gradient of router_topk_fwd's weights;
+    score, normalise and scale as in the forward, ids its choices."""
+    tokens, experts = _two_d(logits, "logits")
+    _check(logits, "logits", dtype=_FLOATS, contiguous=False)
+    _, top_k = _two_d(ids, "ids")
+    _check(ids, "ids", dtype=torch.int32, shape=(tokens, top_k))
+    _check(grad_weights, "grad_weights", dtype=torch.float32, shape=(tokens, top_k))
+    _check(valid_tokens, "valid_tokens", dtype=torch.int32, numel=1)
+    _check(dev_err, "dev_err", dtype=torch.int32, numel=1)
+    with _place(logits.device, stream):
+        if grad_logits is None:
+            grad_logits = torch.empty(tokens, experts, dtype=logits.dtype, device=logits.device)
+        _check(grad_logits, "grad_logits", dtype=logits.dtype, shape=(tokens, experts),
+               contiguous=False)
+        ld, ld_g = _ld(logits, "logits"), _ld(grad_logits, "grad_logits")
+        _cuda(logits, ids, grad_weights, grad_logits, valid_tokens, dev_err)
+        _abi.moe_router_topk_bwd(logits, moe_dtype(logits.dtype), ids, grad_weights, grad_logits,
+                                 valid_tokens, tokens, experts, top_k, ld, ld_g, score, normalise,
+                                 scale, dev_err)
+    return grad_logits
