@@ -6,7 +6,7 @@
  * their dtype variants, the bounded SwiGLU, the fused epilogue chain and the
  * rank-order reduce-scatter), plus the IPC helpers under the reduce-scatter;
  * and the ops of the same block ahead of them: the layer norm and the top-k
- * router, forward and backward.
+ * router, forward and backward, and the whole layer for a few tokens.
  * Each op entry point takes caller-owned DEVICE pointers, sizes and a CUDA
  * stream, validates its arguments on the host, enqueues one kernel (where its
  * comment says so, two or three) on `stream` and returns.
@@ -528,6 +528,57 @@ MOE_API int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t*
                                 int32_t num_experts, int32_t top_k, int64_t ld_logits,
                                 int64_t ld_grad, moe_score score, int normalise, float scale,
                                 int32_t* dev_err, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A whole mixture-of-experts layer for a few tokens (the decode step): router,
+ * both expert products with the clamped SwiGLU between them, combine, shared
+ * expert and residual.
+ *   l = x . router_weight^T, or the logits given; ids, p as moe_router_topk_fwd
+ *   z = w1[e] . x[t],  h = p * silu(min(z_gate, L)) * clamp(z_up, -L, L)
+ *   out[t] = residual[t] + (sum over t's experts, ascending, of w2[e] . h + shared[t])
+ * fp32 from the products to the one rounding to dt; h enters the second product
+ * as the sum of two dt values (its rounding and what that left), so it keeps
+ * 16 bits of mantissa in bf16 and up to 22 in fp16 (in fp16 a finite |h| must stay
+ * below 131008).  The router's product is summed in 64 bits and rounded to fp32, so
+ * that no summation order decides between two experts.  A token's result does
+ * not depend on the other tokens.  A slot without an expert (id -1) adds nothing.
+ * Enqueues two kernels, the second cooperative (one CTA per SM, all resident).
+ * x               dt [tokens, ld_x] (the norm's output), dt MOE_BF16 or MOE_FP16
+ * router_weight   router_dt [num_experts, hidden] contiguous, router_dt dt or
+ *                 MOE_FP32; or NULL with
+ * logits          logits_dt [tokens, ld_logits]: exactly one of the two
+ *                 (MOE_ERR_NULL otherwise)
+ * w1              dt [num_experts, 2 * inter, hidden] contiguous, gate rows first
+ * w2              dt [num_experts, hidden, inter] contiguous
+ * shared_expert_output, residual  dt [tokens, ld_*] or NULL (nothing is added)
+ * out             dt [tokens, ld_out]; may equal residual
+ * topk_weights    fp32 [tokens, top_k] or NULL: the routing weights (output)
+ * topk_ids        int32 [tokens, top_k] or NULL: the chosen experts (output)
+ * valid_tokens    optional int32 (device): rows of every output at or past it
+ *                 stay as they are (MOE_DEVERR_COUNT if outside [0, tokens])
+ * workspace       at least moe_layer_small_batch_workspace() bytes, 256-byte
+ *                 aligned, contents irrelevant before and after; one call at a
+ *                 time may use it
+ * tokens          0 .. 128, tokens * top_k <= 1024;  num_experts 1 .. 512;
+ *                 top_k 1 .. min(32, num_experts);  hidden, inter up to 2^20
+ * limit           as moe_swiglu_clamped_fwd;  score, normalise, scale as
+ *                 moe_router_topk_fwd
+ * dev_err         optional int32 (device): MOE_DEVERR_COUNT; MOE_DEVERR_TIMEOUT
+ *                 if a wait gave up (~1 s)
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_layer_small_batch_workspace(int64_t tokens, int64_t hidden, int64_t inter,
+                                            int32_t num_experts, int32_t top_k, int64_t* bytes);
+MOE_API int moe_layer_small_batch(const void* x, moe_dtype dt, const void* router_weight,
+                                  moe_dtype router_dt, const void* logits, moe_dtype logits_dt,
+                                  const void* w1, const void* w2,
+                                  const void* shared_expert_output, const void* residual,
+                                  void* out, float* topk_weights, int32_t* topk_ids,
+                                  const int32_t* valid_tokens, void* workspace,
+                                  int64_t workspace_bytes, int64_t tokens, int64_t hidden,
+                                  int64_t inter, int32_t num_experts, int32_t top_k, int64_t ld_x,
+                                  int64_t ld_logits, int64_t ld_shared, int64_t ld_residual,
+                                  int64_t ld_out, moe_score score, int normalise, float scale,
+                                  float limit, int32_t* dev_err, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Test hook of the failure path of the bounded waits (no counterpart on the

@@ -52,6 +52,10 @@ SIGNATURES = {
     "moe_router_topk_fwd": [_P, _I, _P, _P, _P, _I64, _I32, _I32, _I64, _I, _I, _F, _P, _P],
     "moe_router_topk_bwd": [_P, _I, _P, _P, _P, _P, _I64, _I32, _I32, _I64, _I64, _I, _I, _F, _P,
                             _P],
+    "moe_layer_small_batch_workspace": [_I64, _I64, _I64, _I32, _I32, ctypes.POINTER(_I64)],
+    "moe_layer_small_batch": [_P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
+                              _I64, _I64, _I64, _I32, _I32, _I64, _I64, _I64, _I64, _I64, _I, _I,
+                              _F, _F, _P, _P],
     "moe_symm_alloc": [ctypes.c_size_t, ctypes.POINTER(_P)],
     "moe_symm_free": [_P],
     "moe_ipc_export": [_P, ctypes.c_char_p],
@@ -259,6 +263,27 @@ def moe_router_topk_bwd(logits, dt, ids, grad_weights, grad_logits, valid_tokens
     _call("moe_router_topk_bwd", ptr(logits), dt, ptr(ids), ptr(grad_weights), ptr(grad_logits),
           ptr(valid_tokens), tokens, num_experts, top_k, ld_logits, ld_grad, score,
           int(bool(normalise)), float(scale), ptr(dev_err), stream_handle(stream))
+
+
+def moe_layer_small_batch_workspace(tokens, hidden, inter, num_experts, top_k) -> int:
+    """Bytes of workspace that moe_layer_small_batch needs."""
+    v = _I64(0)
+    _call("moe_layer_small_batch_workspace", tokens, hidden, inter, num_experts, top_k,
+          ctypes.byref(v))
+    return int(v.value)
+
+
+def moe_layer_small_batch(x, dt, router_weight, router_dt, logits, logits_dt, w1, w2,
+                          shared_expert_output, residual, out, topk_weights, topk_ids,
+                          valid_tokens, workspace, workspace_bytes, tokens, hidden, inter,
+                          num_experts, top_k, ld_x, ld_logits, ld_shared, ld_residual, ld_out,
+                          score, normalise, scale, limit, dev_err=None, stream=None):
+    _call("moe_layer_small_batch", ptr(x), dt, ptr(router_weight), router_dt, ptr(logits),
+          logits_dt, ptr(w1), ptr(w2), ptr(shared_expert_output), ptr(residual), ptr(out),
+          ptr(topk_weights), ptr(topk_ids), ptr(valid_tokens), ptr(workspace), workspace_bytes,
+          tokens, hidden, inter, num_experts, top_k, ld_x, ld_logits, ld_shared, ld_residual,
+          ld_out, score, int(bool(normalise)), float(scale), float(limit), ptr(dev_err),
+          stream_handle(stream))
 
 
 def moe_symm_alloc(nbytes: int) -> int:

@@ -529,4 +529,62 @@ int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t* ids,
                                 stream);
 }
 
+int moe_layer_small_batch_workspace(int64_t tokens, int64_t hidden, int64_t inter,
+                                    int32_t num_experts, int32_t top_k, int64_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  if (!moe_layer_shape_ok(tokens, hidden, inter, num_experts, top_k)) return MOE_ERR_SHAPE;
+  *bytes = moe_layer_workspace(tokens, hidden, inter, num_experts, top_k);
+  return MOE_OK;
+}
+
+int moe_layer_small_batch(const void* x, moe_dtype dt, const void* router_weight,
+                          moe_dtype router_dt, const void* logits, moe_dtype logits_dt,
+                          const void* w1, const void* w2, const void* shared_expert_output,
+                          const void* residual, void* out, float* topk_weights,
+                          int32_t* topk_ids, const int32_t* valid_tokens, void* workspace,
+                          int64_t workspace_bytes, int64_t tokens, int64_t hidden, int64_t inter,
+                          int32_t num_experts, int32_t top_k, int64_t ld_x, int64_t ld_logits,
+                          int64_t ld_shared, int64_t ld_residual, int64_t ld_out,
+                          moe_score score, int normalise, float scale, float limit,
+                          int32_t* dev_err, cudaStream_t stream) {
+  if ((dt != MOE_BF16 && dt != MOE_FP16) || !score_ok(score)) return MOE_ERR_DTYPE;
+  if ((router_weight && router_dt != dt && router_dt != MOE_FP32) ||
+      (logits && !dtype_ok(logits_dt)))
+    return MOE_ERR_DTYPE;
+  if (!moe_layer_shape_ok(tokens, hidden, inter, num_experts, top_k) || ld_x < hidden ||
+      ld_out < hidden || (logits && ld_logits < num_experts) ||
+      (shared_expert_output && ld_shared < hidden) || (residual && ld_residual < hidden) ||
+      !product_ok(tokens, ld_x) || !product_ok(tokens, ld_out) ||
+      (logits && !product_ok(tokens, ld_logits)) ||
+      (shared_expert_output && !product_ok(tokens, ld_shared)) ||
+      (residual && !product_ok(tokens, ld_residual)))
+    return MOE_ERR_SHAPE;
+  if (!limit_ok(limit) || !std::isfinite(scale)) return MOE_ERR_LIMIT;
+  if (tokens == 0 || hidden == 0) return MOE_OK;
+  if (!x || !out || !workspace || (router_weight == nullptr) == (logits == nullptr) ||
+      (inter > 0 && (!w1 || !w2)))
+    return MOE_ERR_NULL;
+  if (workspace_bytes < moe_layer_workspace(tokens, hidden, inter, num_experts, top_k))
+    return MOE_ERR_SHAPE;
+  if (!aligned_to(x, 2) || !aligned_to(w1, 2) || !aligned_to(w2, 2) || !aligned_to(out, 2) ||
+      !aligned_to(shared_expert_output, 2) || !aligned_to(residual, 2) ||
+      !aligned_to(router_weight, dtype_size(router_dt)) ||
+      !aligned_to(logits, dtype_size(logits_dt)) || !aligned_to(topk_weights, 4) ||
+      !aligned_to(topk_ids, 4) || !aligned_to(valid_tokens, 4) || !aligned_to(dev_err, 4) ||
+      !aligned_to(workspace, 256))
+    return MOE_ERR_ALIGN;
+  MoeLayerArgs m = {};
+  m.x = x; m.router_w = router_weight; m.logits = logits; m.w1 = w1; m.w2 = w2;
+  m.shared = shared_expert_output; m.residual = residual; m.out = out; m.workspace = workspace;
+  m.topk_weights = topk_weights; m.topk_ids = topk_ids; m.valid = valid_tokens;
+  m.tokens = (int)tokens; m.hidden = (int)hidden; m.inter = (int)inter;
+  m.E = num_experts; m.K = top_k;
+  m.ld_x = ld_x; m.ld_logits = ld_logits; m.ld_shared = ld_shared; m.ld_residual = ld_residual;
+  m.ld_out = ld_out;
+  m.dt = dt; m.router_dt = router_dt; m.logits_dt = logits_dt;
+  m.softmax = score == MOE_SCORE_SOFTMAX; m.normalise = normalise != 0;
+  m.scale = scale; m.limit = limit; m.err = dev_err;
+  return launch_moe_layer(m, stream);
+}
+
 }  // extern "C"

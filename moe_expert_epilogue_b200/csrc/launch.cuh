@@ -141,4 +141,22 @@ int launch_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t* ids,
                            int64_t ld, int64_t ld_g, bool softmax, bool normalise, float scale,
                            int32_t* err, cudaStream_t stream);
 
+// Arguments of the few-token expert layer (moe_layer_small_batch).
+struct MoeLayerArgs {
+  const void *x, *router_w, *logits, *w1, *w2, *shared, *residual;
+  void *out, *workspace;
+  float* topk_weights;
+  int32_t* topk_ids;
+  const int32_t* valid;
+  int tokens, hidden, inter, E, K;
+  int64_t ld_x, ld_logits, ld_shared, ld_residual, ld_out;
+  moe_dtype dt, router_dt, logits_dt;
+  bool softmax, normalise;
+  float scale, limit;
+  int32_t* err;
+};
+bool moe_layer_shape_ok(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K);
+int64_t moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K);
+int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream);
+
 }  // namespace moe

@@ -474,3 +474,68 @@ def router_topk_bwd(logits, ids, grad_weights, score=MOE_SCORE_SOFTMAX, normalis
                                  valid_tokens, tokens, experts, top_k, ld, ld_g, score, normalise,
                                  scale, dev_err)
     return grad_logits
+
+
+def moe_layer_small_batch(x, w1, w2, top_k, router_weight=None, logits=None,
+                          score=MOE_SCORE_SOFTMAX, normalise=True, scale=1.0,
+                          limit=float("inf"), shared_expert_output=None, residual=None,
+                          valid_tokens=None, out=None, topk_weights=None, topk_ids=None,
+                          workspace=None, dev_err=None, stream=None):
+    """A whole mixture-of-experts layer for up to 128 tokens (bf16 or fp16):
+    out = residual + (sum over each token's experts of its routing weight times
+    w2[e] (clamped SwiGLU of w1[e] x) + shared_expert_output).
+
+    x [tokens, hidden]; w1 [experts, 2*inter, hidden] (gate rows first);
+    w2 [experts, hidden, inter]; router_weight [experts, hidden] (x's dtype or fp32)
+    or logits [tokens, experts]; score, normalise and scale as router_topk_fwd; limit
+    as swiglu_clamped_fwd.  topk_weights (fp32) and topk_ids (int32), [tokens, top_k],
+    receive the choice if given.  Rows at or past valid_tokens (int32 [1] on the
+    device) stay as they are.  out may be residual.  workspace (uint8, 256-byte
+    aligned, at least moe_layer_small_batch_workspace bytes) is allocated unless given."""
+    tokens, hidden = _two_d(x, "x")
+    _check(x, "x", dtype=(torch.bfloat16, torch.float16), contiguous=False)
+    dt = x.dtype
+    if w1.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w1 and w2 must be 3-D: one matrix per expert")
+    experts, two_i, _ = w1.shape
+    if two_i % 2:
+        raise ValueError("w1 must hold [gate; up]: an even number of rows")
+    inter = two_i // 2
+    _check(w1, "w1", dtype=dt, shape=(experts, two_i, hidden))
+    _check(w2, "w2", dtype=dt, shape=(experts, hidden, inter))
+    if (router_weight is None) == (logits is None):
+        raise ValueError("give either router_weight or logits")
+    _check(router_weight, "router_weight", dtype=(dt, torch.float32), shape=(experts, hidden))
+    _check(logits, "logits", dtype=_FLOATS, shape=(tokens, experts), contiguous=False)
+    for t, name in ((shared_expert_output, "shared_expert_output"), (residual, "residual")):
+        _check(t, name, dtype=dt, shape=(tokens, hidden), contiguous=False)
+    _check(valid_tokens, "valid_tokens", dtype=torch.int32, numel=1)
+    _check(topk_weights, "topk_weights", dtype=torch.float32, shape=(tokens, top_k))
+    _check(topk_ids, "topk_ids", dtype=torch.int32, shape=(tokens, top_k))
+    _check(dev_err, "dev_err", dtype=torch.int32, numel=1)
+    with _place(x.device, stream):
+        if out is None:
+            out = torch.empty(tokens, hidden, dtype=dt, device=x.device)
+        _check(out, "out", dtype=dt, shape=(tokens, hidden), contiguous=False)
+        if workspace is None:
+            nbytes = moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        _check(workspace, "workspace", dtype=torch.uint8)
+        _cuda(x, w1, w2, router_weight, logits, shared_expert_output, residual, valid_tokens, out,
+              topk_weights, topk_ids, workspace, dev_err)
+        _abi.moe_layer_small_batch(
+            x, moe_dtype(dt), router_weight,
+            MOE_FP32 if router_weight is None else moe_dtype(router_weight.dtype), logits,
+            MOE_FP32 if logits is None else moe_dtype(logits.dtype), w1, w2, shared_expert_output,
+            residual, out, topk_weights, topk_ids, valid_tokens, workspace, workspace.numel(),
+            tokens, hidden, inter, experts, top_k, _ld(x, "x"),
+            0 if logits is None else _ld(logits, "logits"),
+            0 if shared_expert_output is None else _ld(shared_expert_output, "shared_expert_output"),
+            0 if residual is None else _ld(residual, "residual"), _ld(out, "out"), score,
+            normalise, scale, limit, dev_err)
+    return out
+
+
+def moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k) -> int:
+    """Bytes of workspace of moe_layer_small_batch."""
+    return _abi.moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k)

@@ -161,3 +161,72 @@ def test_router_tensors():
     with pytest.raises(TypeError, match="dtype"):
         ops.router_topk_bwd(logits, ids, gw, grad_logits=z(4, 64))
     _device_error(lambda: ops.router_topk_bwd(logits, ids, gw))
+
+
+def test_moe_layer_status():
+    size = _abi.moe_layer_small_batch_workspace
+    assert size(0, 64, 32, 4, 2) >= 256
+    n = size(4, 64, 32, 8, 2)
+    # logits, the two halves of the activation, the experts' rows
+    assert n >= 256 + 4 * 8 * 4 + 4 * 2 * 2 * 32 * 2 + 4 * 2 * 64 * 4
+    for bad in ((-1, 64, 32, 8, 2), (129, 64, 32, 8, 2), (128, 64, 32, 16, 9), (4, -1, 32, 8, 2),
+                (4, 64, -1, 8, 2), (4, 64, 32, 0, 1), (4, 64, 32, 513, 2), (4, 64, 32, 8, 0),
+                (4, 64, 32, 8, 9), (4, 64, 32, 40, 33), (4, 2 ** 20 + 1, 32, 8, 2)):
+        assert _status(size, *bad) == _abi.MOE_ERR_SHAPE
+
+    def call(x=FAKE, dt=BF16, rw=FAKE, rdt=BF16, logits=None, ldt=FP32, w1=FAKE, w2=FAKE,
+             shared=FAKE, residual=FAKE, out=FAKE, tw=FAKE, ti=FAKE, valid=FAKE, ws=FAKE, nbytes=n,
+             tokens=4, hidden=64, inter=32, experts=8, top_k=2, ld_x=64, ld_l=8, ld_s=64, ld_r=64,
+             ld_o=64, score=0, scale=1.0, limit=7.0, err=None):
+        return _status(_abi.moe_layer_small_batch, x, dt, rw, rdt, logits, ldt, w1, w2, shared,
+                       residual, out, tw, ti, valid, ws, nbytes, tokens, hidden, inter, experts,
+                       top_k, ld_x, ld_l, ld_s, ld_r, ld_o, score, True, scale, limit, err, 0)
+
+    assert call(dt=FP32) == call(score=3) == call(rdt=FP16) == _abi.MOE_ERR_DTYPE
+    assert call(rw=None, logits=FAKE, ldt=5) == _abi.MOE_ERR_DTYPE
+    assert call(tokens=129) == call(experts=600) == call(top_k=9) == call(ld_x=63) == \
+        call(ld_o=63) == call(ld_s=63) == call(ld_r=63) == call(nbytes=n - 1) == _abi.MOE_ERR_SHAPE
+    assert call(rw=None, logits=FAKE, ld_l=7) == _abi.MOE_ERR_SHAPE
+    assert call(limit=0.0) == call(limit=float("nan")) == call(scale=float("inf")) == \
+        _abi.MOE_ERR_LIMIT
+    for k in ("x", "rw", "w1", "w2", "out", "ws"):
+        assert call(**{k: None}) == _abi.MOE_ERR_NULL
+    assert call(logits=FAKE) == _abi.MOE_ERR_NULL          # both sources of the choice
+    for k in ("x", "rw", "w1", "w2", "shared", "residual", "out", "tw", "ti", "valid", "ws", "err"):
+        assert call(**{k: FAKE + 1}) == _abi.MOE_ERR_ALIGN
+    assert call(ws=FAKE + 128) == call(rw=FAKE + 2, rdt=FP32) == _abi.MOE_ERR_ALIGN
+    _abi.moe_layer_small_batch(None, BF16, None, BF16, None, FP32, None, None, None, None, None,
+                               None, None, None, None, 0, 0, 64, 32, 8, 2, 64, 8, 0, 0, 64, 0,
+                               True, 1.0, 7.0, None, 0)
+
+
+def test_moe_layer_tensors():
+    x, w1, w2, rw = z(4, 64), z(8, 64, 64), z(8, 64, 32), z(8, 64)
+    f = ops.moe_layer_small_batch
+    with pytest.raises(TypeError, match="dtype"):
+        f(x.float(), w1, w2, 2, router_weight=rw)
+    with pytest.raises(ValueError, match="3-D"):
+        f(x, w1[0], w2, 2, router_weight=rw)
+    with pytest.raises(ValueError, match="even"):
+        f(x, w1[:, :63], w2, 2, router_weight=rw)
+    with pytest.raises(ValueError, match="shape"):
+        f(x, w1, w2[:, :, :31].contiguous(), 2, router_weight=rw)
+    with pytest.raises(ValueError, match="contiguous"):
+        f(x, w1, z(8, 32, 64).transpose(1, 2), 2, router_weight=rw)
+    with pytest.raises(ValueError, match="either"):
+        f(x, w1, w2, 2)
+    with pytest.raises(ValueError, match="either"):
+        f(x, w1, w2, 2, router_weight=rw, logits=z(4, 8))
+    with pytest.raises(ValueError, match="shape"):
+        f(x, w1, w2, 2, router_weight=z(7, 64))
+    with pytest.raises(ValueError, match="shape"):
+        f(x, w1, w2, 2, logits=z(4, 7, dtype=f32))
+    with pytest.raises(TypeError, match="dtype"):
+        f(x, w1, w2, 2, router_weight=rw, residual=z(4, 64, dtype=f32))
+    with pytest.raises(ValueError, match="shape"):
+        f(x, w1, w2, 2, router_weight=rw, topk_ids=z(4, 3, dtype=i32))
+    with pytest.raises(ValueError, match="shape"):
+        f(x, w1, w2, 2, router_weight=rw, out=z(4, 65))
+    with pytest.raises(_abi.MoeError, match="SHAPE"):
+        f(z(129, 64), w1, w2, 2, router_weight=rw)
+    _device_error(lambda: f(x, w1, w2, 2, router_weight=rw))
