@@ -11,6 +11,23 @@
 // kernel with one CTA per SM for everything else, its phases separated by grid
 // barriers: choice (every CTA makes the same tables for itself), first product
 // and activation, second product, combine.
+//
+// The products.  A work item is a tile of weight rows of one unit (an expert and
+// up to 32 of its tokens); the weights are the 16-row operand of
+// mma.m16n8k16 and the tokens its 8 columns, so one pass over the weights serves
+// all of the unit's tokens.  Four producer warps copy 32 KB of weights at a time
+// and the tokens' matching columns into a ring of shared-memory stages
+// (cp.async); eight consumer warps multiply.  The producers run ahead of the
+// barrier between the products: the second product's first stages of weights are
+// fetched while the slowest CTA finishes the first.
+//
+// The summation order is the same however a product is tiled: the axis is cut
+// into blocks of 256, block c's halves of 128 are accumulated in order into the
+// partial sums (c mod 4, half), and these eight are added in a fixed tree.  A
+// tile of 64 rows holds the four block classes in registers and lets four warps
+// share a block half; a tile of 16 rows gives each of the eight partial sums to
+// a warp.  The small tile is for few items: with 64-row tiles one token's 8 x 64
+// tiles leave a seventh of 148 CTAs idle in the last round.
 #include <math.h>
 
 #include <type_traits>
@@ -42,9 +59,11 @@ struct Tables {
   uint16_t position[kMaxSlots];  // slot -> position
   uint8_t rank[kMaxSlots];       // by slot: k-th place -> k of the token's place-th lowest expert
   uint8_t live[kMaxTokens];      // live slots of a token
+  uint8_t token[kMaxSlots];      // by position
   uint16_t count[kMaxLayerExperts], first[kMaxLayerExperts];
   Unit unit[kMaxUnits];
   int units;
+  int most;                      // tokens of the largest unit
   int tokens;
 };
 
@@ -58,13 +77,14 @@ struct Layer {
   int tokens, hidden, inter, E, K;
   int64_t ld_x, ld_logits, ld_shared, ld_residual, ld_out;
   int logits_dt;
-  bool router_f32, softmax, normalise;
+  bool router_f32, softmax, normalise, aligned_x, aligned_w1, aligned_w2;
   float scale, limit;
   int32_t* err;
   // workspace
   unsigned* barrier;     // [kBarriers]
   float* own_logits;     // [tokens, E]
-  uint16_t* h;           // [slots, 2, inter]: the activation's high and low halves
+  uint16_t* h;           // [slots, 2, ld_h]: the activation's high and low halves
+  int ld_h;              // inter, up to a multiple of 8
   float* y;              // [slots, hidden]
 };
 
@@ -168,10 +188,11 @@ __device__ void make_tables(const Layer& a, Tables& tb, int threads) {
       __syncwarp();
     }
     // the experts' first positions and units
-    int base = 0, units = 0;
+    int base = 0, units = 0, most = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane, n = e < a.E ? tb.count[e] : 0;
       const int u = (n + kUnitTokens - 1) / kUnitTokens;
+      most = max(most, min(n, kUnitTokens));
       int sn = n, su = u;                                   // inclusive prefix sums
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -188,7 +209,11 @@ __device__ void make_tables(const Layer& a, Tables& tb, int threads) {
       base += __shfl_sync(kAll, sn, 31);
       units += __shfl_sync(kAll, su, 31);
     }
-    if (lane == 0) tb.units = units;
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 0) {
+      tb.units = units;
+      tb.most = most;
+    }
     __syncwarp();
     for (int s = lane; s < slots; s += 32) {
       const int e = tb.expert[s];
@@ -196,29 +221,48 @@ __device__ void make_tables(const Layer& a, Tables& tb, int threads) {
         const int p = tb.first[e] + tb.position[s];
         tb.position[s] = (uint16_t)p;
         tb.order[p] = (uint16_t)s;
+        tb.token[p] = (uint8_t)(s / a.K);
       }
     }
   }
   __syncthreads();
 }
 
-// ------------------------------------------------------------ grid barrier
+// ------------------------------------------------------------ waits
 
-// All CTAs' writes before are visible to all CTAs after.  The launch is
-// cooperative, so every CTA is resident; the wait is bounded all the same.
-// Called by one thread between two CTA barriers; false: gave up.
-__device__ __forceinline__ bool grid_arrive_and_wait(unsigned* word, int32_t* err) {
+// Every wait gives up after kWaitCycles: the waiter reports it and sets the
+// CTA's flag, and from then on nobody in the CTA waits, so that the kernel runs
+// to its end (its results are void) with every CTA barrier met.
+
+struct GiveUp {
+  volatile int* flag;   // shared memory
+  int32_t* err;
+  __device__ __forceinline__ bool now(long long t0) const {
+    if (*flag) return true;
+    if (clock64() - t0 <= tma::kWaitCycles) return false;
+    *flag = 1;
+    flag_error(err, MOE_DEVERR_TIMEOUT);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, const GiveUp& g) {
+  if (tma::mbar_try(bar, parity)) return;
+  const long long t0 = clock64();
+  while (!tma::mbar_try(bar, parity) && !g.now(t0)) {}
+}
+
+// Grid barrier, in two parts.  The launch is cooperative: all CTAs are resident.
+__device__ __forceinline__ void grid_arrive(unsigned* word) {
   __threadfence();
   atomicAdd(word, 1u);
+}
+__device__ __forceinline__ void grid_wait(unsigned* word, const GiveUp& g) {
   const long long t0 = clock64();
   while (true) {
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
-    if (v >= gridDim.x) return true;
-    if (clock64() - t0 > tma::kWaitCycles) {
-      flag_error(err, MOE_DEVERR_TIMEOUT);
-      return false;
-    }
+    if (v >= gridDim.x || g.now(t0)) return;
   }
 }
 
@@ -230,7 +274,8 @@ __device__ __forceinline__ float activation(float g, float u, float p, float L) 
 }
 
 // v as the sum of two values of D: v rounded (no further than the largest
-// finite value), and what that left, rounded.
+// finite value), and what that left, rounded.  One rounding alone (2^-9 of
+// each term on average) would cost as much accuracy as the output's.
 template <class D>
 __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
   constexpr float kMax = std::is_same<D, F16>::value ? 65504.0f : 0x1.fep127f;
@@ -240,90 +285,443 @@ __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
   store1<D>(lo, inf ? 0.0f : v - h);
 }
 
-// The coherent load of a value that another CTA wrote before a grid barrier.
+// The load of a value that another CTA wrote before a grid barrier.
 __device__ __forceinline__ float ld_cg(const float* p) {
   float v;
   asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ uint16_t ld_cg(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
-  return v;
+
+constexpr int kConsumers = 8, kProducers = 4;                    // warps
+constexpr int kLayerThreads = (kConsumers + kProducers) * 32;
+constexpr int kSplitCols = 256;                                  // a block of the axis
+constexpr int kMaxStages = 8;
+constexpr int kRedBytes = 4 * 4 * 32 * 16;                       // one buffer of partial sums
+
+// A tile's shape: 64 rows by 256 columns or 16 by 1024 (32 KB of weights).
+struct Tile {
+  int rows, cols, pitch, a_bytes, stage_bytes, stages;
+};
+
+constexpr int kRingBytes = (232448 - (int)sizeof(Tables) - 2 * kRedBytes - 256) / 128 * 128;
+
+__device__ __forceinline__ Tile tile_shape(const Layer& a, const Tables& tb) {
+  Tile t;
+  const int tiles64 = (2 * a.inter + 63) / 64;
+  const bool wide = tb.most > 8 || (int64_t)tb.units * tiles64 >= 8 * (int64_t)gridDim.x;
+  t.rows = wide ? 64 : 16;
+  t.cols = wide ? kSplitCols : 4 * kSplitCols;
+  t.pitch = t.cols * 2 + 16;          // an odd multiple of 16 bytes: ldmatrix without conflicts
+  t.a_bytes = t.rows * t.pitch;
+  t.stage_bytes = t.a_bytes + 2 * tb.most * t.pitch;
+  t.stages = min(kMaxStages, kRingBytes / t.stage_bytes);
+  return t;
+}
+
+struct Ring {
+  uint8_t* base;
+  uint64_t *full, *empty;
+};
+
+// A place in the ring: the slot and the parity of its current use.
+struct Slot {
+  int at;
+  uint32_t parity;
+  __device__ __forceinline__ void next(int stages) {
+    if (++at == stages) { at = 0; parity ^= 1u; }
+  }
+};
+
+// The stages of one CTA's items of a product, in order.
+struct Walk {
+  int item, chunk;
+  __device__ __forceinline__ void next(int chunks) {
+    if (++chunk == chunks) { chunk = 0; item += gridDim.x; }
+  }
+};
+
+struct Product {
+  int axis;      // columns of the weights
+  int tiles;     // row tiles of an expert
+  int items;     // units x tiles
+  int chunks;    // stages per item
+};
+
+__device__ __forceinline__ Product make_product(const Layer& a, const Tables& tb, const Tile& t,
+                                                bool second) {
+  Product p;
+  p.axis = second ? a.inter : a.hidden;
+  p.tiles = second ? (a.hidden + t.rows - 1) / t.rows : (2 * a.inter + t.rows - 1) / t.rows;
+  p.items = tb.units * p.tiles;
+  p.chunks = max(1, (p.axis + t.cols - 1) / t.cols);   // an empty axis: one empty stage, sums of 0
+  return p;
+}
+
+// ---- producers
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tma::smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Eight elements at `col` of a row of `len` columns into shared memory, zeros
+// past the end; element by element where 16-byte copies are not possible.
+template <bool FAST>
+__device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, int col, int len) {
+  if constexpr (FAST) {
+    cp_async16(dst, row + (col < len ? col : 0), col < len ? 16u : 0u);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = col + 2 * i;
+      const uint32_t lo = c < len ? __ldcg(row + c) : 0u;
+      const uint32_t hi = c + 1 < len ? __ldcg(row + c + 1) : 0u;
+      w[i] = lo | hi << 16;
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+}
+
+// Weight rows of one stage.  First product: a tile's 16-row groups hold 8 gate
+// rows and the 8 up rows of the same columns of the activation.
+template <bool SECOND, bool FAST>
+__device__ __forceinline__ void fill_weights(const Layer& a, const Tables& tb, const Tile& t,
+                                             const Product& p, const Walk& w, uint32_t stage,
+                                             int tid) {
+  const Unit u = tb.unit[w.item / p.tiles];
+  const int tile = w.item % p.tiles;
+  const int k0 = w.chunk * t.cols, len = min(t.cols, p.axis - k0);
+  const int pieces = t.cols / 8;                   // 32 or 128: a power of two
+  const int used = (len + 15) / 16 * 2;            // up to a whole k-step
+  const auto* base = static_cast<const uint16_t*>(SECOND ? a.w2 : a.w1);
+#pragma unroll 8
+  for (int i = tid; i < t.rows * pieces; i += kProducers * 32) {
+    const int r = i / pieces, c = i % pieces;
+    int64_t row;
+    bool live;
+    if (SECOND) {
+      const int col = tile * t.rows + r;
+      live = col < a.hidden;
+      row = (int64_t)u.expert * a.hidden + col;
+    } else {
+      const int j = tile * (t.rows / 2) + (r >> 4) * 8 + (r & 7);
+      live = j < a.inter;
+      row = ((int64_t)u.expert * 2 + ((r >> 3) & 1)) * a.inter + j;
+    }
+    if (live && c < used) copy8<FAST>(stage + r * t.pitch + c * 16, base + row * p.axis + k0, c * 8,
+                                      len);
+  }
+}
+
+// The matching columns of the unit's tokens (first product), or of both halves
+// of their activations (second).
+template <bool SECOND, bool FAST>
+__device__ __forceinline__ void fill_tokens(const Layer& a, const Tables& tb, const Tile& t,
+                                            const Product& p, const Walk& w, uint32_t stage,
+                                            int tid) {
+  const Unit u = tb.unit[w.item / p.tiles];
+  const int k0 = w.chunk * t.cols, len = min(t.cols, p.axis - k0);
+  const int pieces = t.cols / 8, used = (len + 15) / 16 * 2;
+  const int rows = SECOND ? 2 * u.count : u.count;
+  stage += t.a_bytes;
+  for (int i = tid; i < rows * pieces; i += kProducers * 32) {
+    const int r = i / pieces, c = i % pieces;
+    const uint16_t* src;
+    if (SECOND) {
+      const int n = r < u.count ? r : r - u.count;
+      src = a.h + ((int64_t)(u.first + n) * 2 + (r < u.count ? 0 : 1)) * a.ld_h + k0;
+    } else {
+      src = static_cast<const uint16_t*>(a.x) + tb.token[u.first + r] * a.ld_x + k0;
+    }
+    // (the activation's rows are padded to 8 elements, whose surplus is zero)
+    if (c < used) copy8<FAST>(stage + r * t.pitch + c * 16, src, c * 8, len);
+  }
+}
+
+template <bool FAST>
+__device__ __forceinline__ void stage_done(uint64_t* full) {
+  if constexpr (FAST) {
+    cp_async_arrive(full);
+  } else {
+    cp_async_wait();
+    tma::mbar_arrive(full);
+  }
+}
+
+template <bool SECOND, bool FAST>
+__device__ __forceinline__ void produce(const Layer& a, const Tables& tb, const Tile& t,
+                                        const Product& p, const Ring& ring, Slot& slot,
+                                        int& unused, const GiveUp& g, int tid) {
+  Walk w{(int)blockIdx.x, 0};
+  auto claim = [&] {                     // wait until the slot may be overwritten
+    if (unused > 0) --unused;
+    else wait_phase(&ring.empty[slot.at], slot.parity ^ 1u, g);
+    return tma::smem_addr(ring.base + (size_t)slot.at * t.stage_bytes);
+  };
+  if (SECOND) {
+    // weights ahead of the barrier, then the activations they meet
+    Walk ahead = w;
+    Slot first = slot;
+    int n = 0;
+    for (; n < t.stages && ahead.item < p.items; ++n) {
+      fill_weights<SECOND, FAST>(a, tb, t, p, ahead, claim(), tid);
+      ahead.next(p.chunks);
+      slot.next(t.stages);
+    }
+    if ((tid & 31) == 0) grid_wait(&a.barrier[0], g);
+    __syncwarp();
+    for (; n > 0; --n) {
+      fill_tokens<true, true>(a, tb, t, p, w,
+                              tma::smem_addr(ring.base + (size_t)first.at * t.stage_bytes), tid);
+      stage_done<FAST>(&ring.full[first.at]);
+      w.next(p.chunks);
+      first.next(t.stages);
+    }
+  }
+  while (w.item < p.items) {
+    const uint32_t stage = claim();
+    fill_weights<SECOND, FAST>(a, tb, t, p, w, stage, tid);
+    fill_tokens<SECOND, SECOND || FAST>(a, tb, t, p, w, stage, tid);
+    stage_done<FAST>(&ring.full[slot.at]);
+    w.next(p.chunks);
+    slot.next(t.stages);
+  }
+}
+
+// ---- consumers
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 template <class D>
-__device__ __forceinline__ float widen1(uint16_t v);
-template <> __device__ __forceinline__ float widen1<BF16>(uint16_t v) {
-  return __uint_as_float((uint32_t)v << 16);
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<D, BF16>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <> __device__ __forceinline__ float widen1<F16>(uint16_t v) { return f16_to_f32(v); }
+
+// This warp's 128 columns of one stage: acc[j] += weights (16 rows) x tokens
+// 8 j .. 8 j + 7.  Columns past the unit's last token repeat it; nothing reads
+// their sums.
+template <class D, bool SECOND, int NT>
+__device__ __forceinline__ void multiply(float (&acc)[NT][4], uint32_t wrow, uint32_t trow,
+                                         const uint32_t (&boff)[NT], uint32_t lo_off, int ksteps,
+                                         int nt) {
+#pragma unroll
+  for (int kp = 0; kp < 4; ++kp) {
+    if (2 * kp >= ksteps) break;
+    uint32_t a0[4], a1[4];
+    ldsm4(a0, wrow + kp * 64);
+    ldsm4(a1, wrow + kp * 64 + 32);       // (within the stage, unused past the last k-step)
+    const bool both = 2 * kp + 1 < ksteps;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j >= nt) break;
+      uint32_t b[4];
+      ldsm4(b, trow + boff[j] + kp * 64);
+      mma16816<D>(acc[j], a0, b[0], b[1]);
+      if (SECOND) {
+        uint32_t l[4];
+        ldsm4(l, trow + boff[j] + lo_off + kp * 64);
+        mma16816<D>(acc[j], a0, l[0], l[1]);
+        if (both) {
+          mma16816<D>(acc[j], a1, b[2], b[3]);
+          mma16816<D>(acc[j], a1, l[2], l[3]);
+        }
+      } else if (both) {
+        mma16816<D>(acc[j], a1, b[2], b[3]);
+      }
+    }
+  }
+}
+
+// Lane (g, q) of a 16 x 8 block of sums: rows g, g + 8, tokens 2 q, 2 q + 1.
+template <class D, bool SECOND>
+__device__ __forceinline__ void finish(const Layer& a, const Tables& tb, const Unit& u, int row0,
+                                       int tok0, int lane, const float (&c)[4]) {
+  const int g = lane >> 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int tok = tok0 + (lane & 3) * 2 + i;
+    if (tok >= u.count) continue;
+    const int pos = u.first + tok;
+    if (SECOND) {
+      float* y = a.y + (int64_t)pos * a.hidden;
+      if (row0 + g < a.hidden) y[row0 + g] = c[i];
+      if (row0 + g + 8 < a.hidden) y[row0 + g + 8] = c[i + 2];
+    } else {
+      const int j = row0 / 2 + g;
+      uint16_t* h = a.h + (int64_t)pos * 2 * a.ld_h + j;
+      if (j < a.inter)
+        split<D>(activation(c[i], c[i + 2], tb.weight[tb.order[pos]], a.limit), h, h + a.ld_h);
+      else if (j < a.ld_h)
+        h[0] = h[a.ld_h] = 0;
+    }
+  }
+}
+
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+
+template <class D, bool WIDE, bool SECOND>
+__device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const Tile& t,
+                                        const Product& p, const Ring& ring, Slot& slot,
+                                        float4* red, int& buffer, const GiveUp& g) {
+  constexpr int NS = WIDE ? 4 : 1, NT = WIDE ? 4 : 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int half = warp >> 2, quarter = warp & 3;
+  const int group = WIDE ? quarter : 0;                       // 16-row group of the tile
+  const int off = (WIDE ? 0 : quarter * kSplitCols) + half * (kSplitCols / 2);
+  const uint32_t ring_base = tma::smem_addr(ring.base);
+  const uint32_t wlane = (group * 16 + (lane & 15)) * t.pitch + (off + (lane >> 4) * 8) * 2;
+  for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    const Unit u = tb.unit[item / p.tiles];
+    const int nt = (u.count + 7) / 8;
+    uint32_t boff[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) boff[j] = min(j * 8 + (lane & 7), u.count - 1) * t.pitch;
+    const uint32_t lo_off = u.count * t.pitch;
+    float acc[NS][NT][4] = {};
+    for (int c0 = 0; c0 < p.chunks; c0 += NS) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (c0 + s >= p.chunks) break;
+        const int len = min(t.cols, p.axis - (c0 + s) * t.cols) - off;
+        const uint32_t stage = ring_base + slot.at * t.stage_bytes;
+        wait_phase(&ring.full[slot.at], slot.parity, g);
+        __syncwarp();
+        multiply<D, SECOND, NT>(acc[s], stage + wlane,
+                                stage + t.a_bytes + (off + (lane >> 3) * 8) * 2, boff, lo_off,
+                                min(8, (len + 15) / 16), nt);
+        __syncwarp();
+        if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
+        slot.next(t.stages);
+      }
+    }
+    // the eight partial sums, in one order: ((0 + 1) + (2 + 3)) of each half, then the halves
+    float4* r = red + buffer * (kRedBytes / 16);
+    const int row0 = (item % p.tiles) * t.rows;
+    if (WIDE) {
+      float sum[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sum[j][i] = (acc[0][j][i] + acc[NS > 1 ? 1 : 0][j][i]) +
+                      (acc[NS > 2 ? 2 : 0][j][i] + acc[NS > 3 ? 3 : 0][j][i]);
+        if (half == 1 && j < nt)
+          r[(group * 4 + j) * 32 + lane] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
+      }
+      consumers_sync();
+      if (half == 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (j >= nt) break;
+          const float4 o = r[(group * 4 + j) * 32 + lane];
+          const float c[4] = {sum[j][0] + o.x, sum[j][1] + o.y, sum[j][2] + o.z, sum[j][3] + o.w};
+          finish<D, SECOND>(a, tb, u, row0 + group * 16, j * 8, lane, c);
+        }
+      }
+    } else {
+      r[warp * 32 + lane] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
+      consumers_sync();
+      // one warp finishes an item, another the next
+      if (warp == (item / (int)gridDim.x) % kConsumers) {
+        float c[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 v0 = r[(h * 4 + 0) * 32 + lane], v1 = r[(h * 4 + 1) * 32 + lane];
+          const float4 v2 = r[(h * 4 + 2) * 32 + lane], v3 = r[(h * 4 + 3) * 32 + lane];
+          c[h][0] = (v0.x + v1.x) + (v2.x + v3.x);
+          c[h][1] = (v0.y + v1.y) + (v2.y + v3.y);
+          c[h][2] = (v0.z + v1.z) + (v2.z + v3.z);
+          c[h][3] = (v0.w + v1.w) + (v2.w + v3.w);
+        }
+        const float s[4] = {c[0][0] + c[1][0], c[0][1] + c[1][1], c[0][2] + c[1][2],
+                            c[0][3] + c[1][3]};
+        finish<D, SECOND>(a, tb, u, row0, 0, lane, s);
+      }
+    }
+    buffer ^= 1;      // the next item's sums must not meet readers of these
+  }
+}
 
 template <class D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kLayerThreads, 1)
 layer_experts(Layer a) {
   __shared__ Tables tb;
+  __shared__ float4 red[2 * kRedBytes / 16];
+  __shared__ uint64_t bars[2 * kMaxStages];
   __shared__ int gave_up;
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kThreads / 32);
-  const int warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const auto* x = static_cast<const uint16_t*>(a.x);
-  const auto* w1 = static_cast<const uint16_t*>(a.w1);
-  const auto* w2 = static_cast<const uint16_t*>(a.w2);
-  if (threadIdx.x == 0) gave_up = 0;
-  make_tables(a, tb, kThreads);
-  // first product: one warp per (unit, column of the activation)
-  const int64_t n1 = (int64_t)tb.units * a.inter;
-  for (int64_t i = warp; i < n1; i += warps) {
-    const Unit u = tb.unit[i / a.inter];
-    const int j = (int)(i % a.inter);
-    const uint16_t* wg = w1 + ((int64_t)u.expert * 2 * a.inter + j) * a.hidden;
-    const uint16_t* wu = wg + (int64_t)a.inter * a.hidden;
-    for (int n = 0; n < u.count; ++n) {
-      const int slot = tb.order[u.first + n];
-      const uint16_t* xr = x + (slot / a.K) * a.ld_x;
-      float g = 0.f, v = 0.f;
-      for (int h = lane; h < a.hidden; h += 32) {
-        const float xv = load1<D>(xr + h);
-        g = fmaf(load1<D>(wg + h), xv, g);
-        v = fmaf(load1<D>(wu + h), xv, v);
-      }
-      g = warp_sum(g);
-      v = warp_sum(v);
-      if (lane == 0) {
-        const float act = activation(g, v, tb.weight[slot], a.limit);
-        uint16_t* hr = a.h + (int64_t)(u.first + n) * 2 * a.inter + j;
-        split<D>(act, hr, hr + a.inter);
-      }
+  extern __shared__ __align__(128) uint8_t ring_mem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Ring ring{ring_mem, bars, bars + kMaxStages};
+  if (threadIdx.x == 0) {
+    gave_up = 0;
+    for (int i = 0; i < kMaxStages; ++i) {
+      tma::mbar_init(&ring.full[i], kProducers * 32);
+      tma::mbar_init(&ring.empty[i], kConsumers);
     }
   }
-  __syncthreads();
-  if (threadIdx.x == 0 && !grid_arrive_and_wait(&a.barrier[0], a.err)) gave_up = 1;
-  __syncthreads();
-  if (gave_up) return;
-  // second product: one warp per (unit, hidden column)
-  const int64_t n2 = (int64_t)tb.units * a.hidden;
-  for (int64_t i = warp; i < n2; i += warps) {
-    const Unit u = tb.unit[i / a.hidden];
-    const int c = (int)(i % a.hidden);
-    const uint16_t* w = w2 + ((int64_t)u.expert * a.hidden + c) * a.inter;
-    for (int n = 0; n < u.count; ++n) {
-      const uint16_t* hr = a.h + (int64_t)(u.first + n) * 2 * a.inter;
-      float s = 0.f;
-      for (int j = lane; j < a.inter; j += 32)
-        s = fmaf(load1<D>(w + j), widen1<D>(ld_cg(hr + j)) + widen1<D>(ld_cg(hr + a.inter + j)), s);
-      s = warp_sum(s);
-      if (lane == 0) a.y[(int64_t)(u.first + n) * a.hidden + c] = s;
-    }
+  make_tables(a, tb, kLayerThreads);
+  const GiveUp g{&gave_up, a.err};
+  const Tile t = tile_shape(a, tb);
+  const Product p1 = make_product(a, tb, t, false), p2 = make_product(a, tb, t, true);
+  Slot slot{0, 0};
+  if (warp >= kConsumers) {
+    const int tid = threadIdx.x - kConsumers * 32;
+    int unused = t.stages;
+    const bool fast1 = a.hidden % 8 == 0 && a.ld_x % 8 == 0 && a.aligned_x && a.aligned_w1;
+    const bool fast2 = a.inter % 8 == 0 && a.aligned_w2;
+    if (fast1) produce<false, true>(a, tb, t, p1, ring, slot, unused, g, tid);
+    else produce<false, false>(a, tb, t, p1, ring, slot, unused, g, tid);
+    if (fast2) produce<true, true>(a, tb, t, p2, ring, slot, unused, g, tid);
+    else produce<true, false>(a, tb, t, p2, ring, slot, unused, g, tid);
+    cp_async_wait();
+    return;
   }
-  __syncthreads();
-  if (threadIdx.x == 0 && !grid_arrive_and_wait(&a.barrier[1], a.err)) gave_up = 1;
-  __syncthreads();
-  if (gave_up) return;
+  int buffer = 0;
+  const bool wide = t.rows == 64;
+  if (wide) consume<D, true, false>(a, tb, t, p1, ring, slot, red, buffer, g);
+  else consume<D, false, false>(a, tb, t, p1, ring, slot, red, buffer, g);
+  consumers_sync();
+  if (threadIdx.x == 0) grid_arrive(&a.barrier[0]);
+  if (wide) consume<D, true, true>(a, tb, t, p2, ring, slot, red, buffer, g);
+  else consume<D, false, true>(a, tb, t, p2, ring, slot, red, buffer, g);
+  consumers_sync();
+  if (threadIdx.x == 0) {
+    grid_arrive(&a.barrier[1]);
+    grid_wait(&a.barrier[1], g);
+  }
+  consumers_sync();
   // combine: the chosen experts of a token in ascending order
   const int64_t total = (int64_t)tb.tokens * a.hidden;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * (kConsumers * 32) + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * (kConsumers * 32)) {
     const int t = (int)(i / a.hidden), c = (int)(i % a.hidden);
     float s = 0.f;
     for (int k = 0; k < tb.live[t]; ++k) {
@@ -350,7 +748,7 @@ Space layer_space(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int6
   Space s;
   s.logits = 256;                                        // the barrier words come first
   s.h = s.logits + up256(tokens * E * 4);
-  s.y = s.h + up256(tokens * K * 2 * inter * 2);
+  s.y = s.h + up256(tokens * K * 2 * ((inter + 7) / 8 * 8) * 2);
   s.bytes = s.y + up256(tokens * K * hidden * 4);
   return s;
 }
@@ -367,8 +765,10 @@ int launch(Layer& a, cudaStream_t stream) {
   if (int rc = device_sm_count(&sms)) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kLayerThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = stream;
+  if (int rc = ensure_smem_limit((const void*)layer_experts<D>, kRingBytes)) return rc;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
@@ -406,6 +806,8 @@ int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream) {
   a.own_logits = reinterpret_cast<float*>(ws + s.logits);
   a.h = reinterpret_cast<uint16_t*>(ws + s.h);
   a.y = reinterpret_cast<float*>(ws + s.y);
+  a.ld_h = (m.inter + 7) / 8 * 8;
+  a.aligned_x = aligned16(m.x); a.aligned_w1 = aligned16(m.w1); a.aligned_w2 = aligned16(m.w2);
   a.logits = m.router_w ? a.own_logits : m.logits;
   a.logits_dt = m.router_w ? MOE_FP32 : m.logits_dt;
   a.ld_logits = m.router_w ? m.E : m.ld_logits;
