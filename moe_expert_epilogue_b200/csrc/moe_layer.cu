@@ -16,8 +16,8 @@
 // up to 32 of its tokens); the weights are the 16-row operand of
 // mma.m16n8k16 and the tokens its 8 columns, so one pass over the weights serves
 // all of the unit's tokens.  Four producer warps copy 32 KB of weights at a time
-// and the tokens' matching columns into a ring of shared-memory stages
-// (cp.async); eight consumer warps multiply.  The producers run ahead of the
+// and the tokens' matching columns into a ring of shared-memory stages (one
+// bulk copy a row); eight consumer warps multiply.  The producers run ahead of the
 // barrier between the products: the second product's first stages of weights are
 // fetched while the slowest CTA finishes the first.
 //
@@ -266,6 +266,11 @@ __device__ __forceinline__ void grid_wait(unsigned* word, const GiveUp& g) {
   }
 }
 
+// Orders this thread's generic accesses against bulk copies.
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
 // ------------------------------------------------------------ products
 
 __device__ __forceinline__ float activation(float g, float u, float p, float L) {
@@ -359,103 +364,66 @@ __device__ __forceinline__ Product make_product(const Layer& a, const Tables& tb
 
 // ---- producers
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tma::smem_addr(bar))
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+// Rows of a stage: the tile's weight rows, then the unit's token rows (of the
+// second product: both halves of their activations).  At most 64 + 2 * 32: each
+// producer thread owns one of them and copies its columns with one bulk copy,
+// where rows start on 16-byte boundaries (FAST); other weights are put together
+// element by element by all producers.
+
+// Weight row r of an item, or null past the last.  First product: a tile's
+// 16-row groups hold 8 gate rows and the 8 up rows of the same columns of the
+// activation.
+template <bool SECOND>
+__device__ __forceinline__ const uint16_t* weight_row(const Layer& a, const Tile& t, const Unit& u,
+                                                      int tile, int r) {
+  if (SECOND) {
+    const int col = tile * t.rows + r;
+    if (col >= a.hidden) return nullptr;
+    return static_cast<const uint16_t*>(a.w2) + ((int64_t)u.expert * a.hidden + col) * a.inter;
+  }
+  const int j = tile * (t.rows / 2) + (r >> 4) * 8 + (r & 7);
+  if (j >= a.inter) return nullptr;
+  return static_cast<const uint16_t*>(a.w1) +
+         (((int64_t)u.expert * 2 + ((r >> 3) & 1)) * a.inter + j) * a.hidden;
 }
 
-// Eight elements at `col` of a row of `len` columns into shared memory, zeros
-// past the end; element by element where 16-byte copies are not possible.
-template <bool FAST>
+template <bool SECOND>
+__device__ __forceinline__ const uint16_t* token_row(const Layer& a, const Tables& tb,
+                                                     const Unit& u, int r) {
+  if (SECOND) {
+    const int n = r < u.count ? r : r - u.count;
+    return a.h + ((int64_t)(u.first + n) * 2 + (r < u.count ? 0 : 1)) * a.ld_h;
+  }
+  return static_cast<const uint16_t*>(a.x) + tb.token[u.first + r] * a.ld_x;
+}
+
+// Columns [col, col + 8) of a row of `len` columns into shared memory, zeros
+// past the end.
 __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, int col, int len) {
-  if constexpr (FAST) {
-    cp_async16(dst, row + (col < len ? col : 0), col < len ? 16u : 0u);
-  } else {
-    uint32_t w[4];
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = col + 2 * i;
-      const uint32_t lo = c < len ? __ldcg(row + c) : 0u;
-      const uint32_t hi = c + 1 < len ? __ldcg(row + c + 1) : 0u;
-      w[i] = lo | hi << 16;
-    }
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3])
-                 : "memory");
+  for (int i = 0; i < 4; ++i) {
+    const int c = col + 2 * i;
+    const uint32_t lo = c < len ? __ldg(row + c) : 0u;
+    const uint32_t hi = c + 1 < len ? __ldg(row + c + 1) : 0u;
+    w[i] = lo | hi << 16;
   }
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3])
+               : "memory");
 }
 
-// Weight rows of one stage.  First product: a tile's 16-row groups hold 8 gate
-// rows and the 8 up rows of the same columns of the activation.
-template <bool SECOND, bool FAST>
-__device__ __forceinline__ void fill_weights(const Layer& a, const Tables& tb, const Tile& t,
-                                             const Product& p, const Walk& w, uint32_t stage,
-                                             int tid) {
-  const Unit u = tb.unit[w.item / p.tiles];
-  const int tile = w.item % p.tiles;
-  const int k0 = w.chunk * t.cols, len = min(t.cols, p.axis - k0);
-  const int pieces = t.cols / 8;                   // 32 or 128: a power of two
-  const int used = (len + 15) / 16 * 2;            // up to a whole k-step
-  const auto* base = static_cast<const uint16_t*>(SECOND ? a.w2 : a.w1);
-#pragma unroll 8
-  for (int i = tid; i < t.rows * pieces; i += kProducers * 32) {
-    const int r = i / pieces, c = i % pieces;
-    int64_t row;
-    bool live;
-    if (SECOND) {
-      const int col = tile * t.rows + r;
-      live = col < a.hidden;
-      row = (int64_t)u.expert * a.hidden + col;
-    } else {
-      const int j = tile * (t.rows / 2) + (r >> 4) * 8 + (r & 7);
-      live = j < a.inter;
-      row = ((int64_t)u.expert * 2 + ((r >> 3) & 1)) * a.inter + j;
-    }
-    if (live && c < used) copy8<FAST>(stage + r * t.pitch + c * 16, base + row * p.axis + k0, c * 8,
-                                      len);
-  }
-}
-
-// The matching columns of the unit's tokens (first product), or of both halves
-// of their activations (second).
-template <bool SECOND, bool FAST>
-__device__ __forceinline__ void fill_tokens(const Layer& a, const Tables& tb, const Tile& t,
-                                            const Product& p, const Walk& w, uint32_t stage,
-                                            int tid) {
-  const Unit u = tb.unit[w.item / p.tiles];
-  const int k0 = w.chunk * t.cols, len = min(t.cols, p.axis - k0);
-  const int pieces = t.cols / 8, used = (len + 15) / 16 * 2;
-  const int rows = SECOND ? 2 * u.count : u.count;
-  stage += t.a_bytes;
-  for (int i = tid; i < rows * pieces; i += kProducers * 32) {
-    const int r = i / pieces, c = i % pieces;
-    const uint16_t* src;
-    if (SECOND) {
-      const int n = r < u.count ? r : r - u.count;
-      src = a.h + ((int64_t)(u.first + n) * 2 + (r < u.count ? 0 : 1)) * a.ld_h + k0;
-    } else {
-      src = static_cast<const uint16_t*>(a.x) + tb.token[u.first + r] * a.ld_x + k0;
-    }
-    // (the activation's rows are padded to 8 elements, whose surplus is zero)
-    if (c < used) copy8<FAST>(stage + r * t.pitch + c * 16, src, c * 8, len);
-  }
-}
-
-template <bool FAST>
-__device__ __forceinline__ void stage_done(uint64_t* full) {
-  if constexpr (FAST) {
-    cp_async_arrive(full);
-  } else {
-    cp_async_wait();
-    tma::mbar_arrive(full);
+// `rows` rows of a stage element by element; row(r) is a row's start at this
+// stage's first column, or null.
+template <class Row>
+__device__ __forceinline__ void copy_rows(uint32_t dst, int rows, int pitch, int len, int tid,
+                                          Row row) {
+  const int pieces = (len + 7) / 8;
+  for (int r = tid >> 5; r < rows; r += kProducers) {
+    const uint16_t* src = row(r);
+    if (!src) continue;
+#pragma unroll 4
+    for (int c = tid & 31; c < pieces; c += 32) copy8(dst + r * pitch + c * 16, src, c * 8, len);
   }
 }
 
@@ -463,39 +431,92 @@ template <bool SECOND, bool FAST>
 __device__ __forceinline__ void produce(const Layer& a, const Tables& tb, const Tile& t,
                                         const Product& p, const Ring& ring, Slot& slot,
                                         int& unused, const GiveUp& g, int tid) {
-  Walk w{(int)blockIdx.x, 0};
+  constexpr bool kFastTokens = SECOND || FAST;   // the workspace's rows are aligned
+  const int lane = tid & 31;
+  // This thread's row of the item, if it copies one.
+  struct Mine { const uint16_t* src; bool weights; };
+  auto mine = [&](int item) {
+    const Unit u = tb.unit[item / p.tiles];
+    Mine m{nullptr, tid < t.rows};
+    if (m.weights) {
+      if (FAST) m.src = weight_row<SECOND>(a, t, u, item % p.tiles, tid);
+    } else if (kFastTokens && tid - t.rows < (SECOND ? 2 : 1) * u.count) {
+      m.src = token_row<SECOND>(a, tb, u, tid - t.rows);
+    }
+    return m;
+  };
   auto claim = [&] {                     // wait until the slot may be overwritten
     if (unused > 0) --unused;
     else wait_phase(&ring.empty[slot.at], slot.parity ^ 1u, g);
-    return tma::smem_addr(ring.base + (size_t)slot.at * t.stage_bytes);
   };
+  // Parts of one stage: copies of weights and / or tokens; `last`: this warp's
+  // arrival, with which the copies announced complete the stage.
+  auto fill = [&](const Walk& w, const Mine& m, int at, bool weights, bool tokens, bool last) {
+    const int k0 = w.chunk * t.cols, len = min(t.cols, p.axis - k0);
+    uint8_t* stage = ring.base + (size_t)at * t.stage_bytes;
+    if (!FAST && weights) {
+      const Unit u = tb.unit[w.item / p.tiles];
+      copy_rows(tma::smem_addr(stage), t.rows, t.pitch, len, tid, [&](int r) {
+        const uint16_t* row = weight_row<SECOND>(a, t, u, w.item % p.tiles, r);
+        return row ? row + k0 : nullptr;
+      });
+      if (!kFastTokens)
+        copy_rows(tma::smem_addr(stage + t.a_bytes), u.count, t.pitch, len, tid,
+                  [&](int r) { return token_row<SECOND>(a, tb, u, r) + k0; });
+      fence_async_proxy();               // later bulk copies into the stage come after
+      __syncwarp();
+    }
+    const bool copies = m.src && len > 0 && (m.weights ? weights : tokens);
+    const uint32_t bytes = SECOND && !FAST ? (len + 7) / 8 * 16 : len * 2;
+    const uint32_t total = __popc(__ballot_sync(kAll, copies)) * bytes;
+    if (lane == 0) {
+      if (last) tma::mbar_arrive_expect_tx(&ring.full[at], total);
+      else if (total) tma::mbar_expect_tx(&ring.full[at], total);
+    }
+    __syncwarp();
+    if (copies) tma::bulk_load(stage + tid * t.pitch, m.src + k0, bytes, &ring.full[at]);
+  };
+  Walk w{(int)blockIdx.x, 0};
+  Mine m{};
   if (SECOND) {
     // weights ahead of the barrier, then the activations they meet
     Walk ahead = w;
     Slot first = slot;
     int n = 0;
     for (; n < t.stages && ahead.item < p.items; ++n) {
-      fill_weights<SECOND, FAST>(a, tb, t, p, ahead, claim(), tid);
+      if (ahead.chunk == 0) m = mine(ahead.item);
+      claim();
+      fill(ahead, m, slot.at, true, false, false);
       ahead.next(p.chunks);
       slot.next(t.stages);
     }
-    if ((tid & 31) == 0) grid_wait(&a.barrier[0], g);
+    if (lane == 0) grid_wait(&a.barrier[0], g);
     __syncwarp();
+    fence_async_proxy();                 // the activations are read by bulk copies
     for (; n > 0; --n) {
-      fill_tokens<true, true>(a, tb, t, p, w,
-                              tma::smem_addr(ring.base + (size_t)first.at * t.stage_bytes), tid);
-      stage_done<FAST>(&ring.full[first.at]);
+      if (w.chunk == 0) m = mine(w.item);
+      fill(w, m, first.at, false, true, true);
       w.next(p.chunks);
       first.next(t.stages);
     }
+    if (w.item < p.items) m = mine(w.item);
   }
   while (w.item < p.items) {
-    const uint32_t stage = claim();
-    fill_weights<SECOND, FAST>(a, tb, t, p, w, stage, tid);
-    fill_tokens<SECOND, SECOND || FAST>(a, tb, t, p, w, stage, tid);
-    stage_done<FAST>(&ring.full[slot.at]);
+    if (w.chunk == 0) m = mine(w.item);
+    claim();
+    fill(w, m, slot.at, true, true, true);
     w.next(p.chunks);
     slot.next(t.stages);
+  }
+}
+
+// Waits until every stage filled has landed: a CTA does not end before its copies.
+__device__ __forceinline__ void drain(const Tile& t, const Ring& ring, const Slot& slot, int unused,
+                                      const GiveUp& g) {
+  for (int i = 0; i < t.stages; ++i) {
+    if (unused > 0 && i >= t.stages - unused) continue;
+    const uint32_t parity = i < slot.at ? slot.parity : slot.parity ^ 1u;
+    if (!tma::mbar_wait(&ring.full[i], parity)) flag_error(g.err, MOE_DEVERR_TIMEOUT);
   }
 }
 
@@ -523,29 +544,38 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// This warp's 128 columns of one stage: acc[j] += weights (16 rows) x tokens
-// 8 j .. 8 j + 7.  Columns past the unit's last token repeat it; nothing reads
-// their sums.
+// This warp's `len` (up to 128) columns of one stage: acc[j] += weights (16
+// rows) x tokens 8 j .. 8 j + 7.  Columns past the unit's last token repeat it;
+// nothing reads their sums.  The axis ends on a multiple of 8 columns: of a last
+// k-step of 16 with 8, the upper half of the fragments is cleared, since what
+// lies there in shared memory may be anything.
 template <class D, bool SECOND, int NT>
 __device__ __forceinline__ void multiply(float (&acc)[NT][4], uint32_t wrow, uint32_t trow,
-                                         const uint32_t (&boff)[NT], uint32_t lo_off, int ksteps,
+                                         const uint32_t (&boff)[NT], uint32_t lo_off, int len,
                                          int nt) {
 #pragma unroll
   for (int kp = 0; kp < 4; ++kp) {
-    if (2 * kp >= ksteps) break;
+    if (kp * 32 >= len) break;
     uint32_t a0[4], a1[4];
     ldsm4(a0, wrow + kp * 64);
     ldsm4(a1, wrow + kp * 64 + 32);       // (within the stage, unused past the last k-step)
-    const bool both = 2 * kp + 1 < ksteps;
+    const bool both = kp * 32 + 16 < len;
+    const bool cut0 = kp * 32 + 8 >= len, cut1 = kp * 32 + 24 >= len;
+    if (cut0) a0[2] = a0[3] = 0;
+    if (cut1) a1[2] = a1[3] = 0;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
       uint32_t b[4];
       ldsm4(b, trow + boff[j] + kp * 64);
+      if (cut0) b[1] = 0;
+      if (cut1) b[3] = 0;
       mma16816<D>(acc[j], a0, b[0], b[1]);
       if (SECOND) {
         uint32_t l[4];
         ldsm4(l, trow + boff[j] + lo_off + kp * 64);
+        if (cut0) l[1] = 0;
+        if (cut1) l[3] = 0;
         mma16816<D>(acc[j], a0, l[0], l[1]);
         if (both) {
           mma16816<D>(acc[j], a1, b[2], b[3]);
@@ -616,7 +646,7 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
         __syncwarp();
         multiply<D, SECOND, NT>(acc[s], stage + wlane,
                                 stage + t.a_bytes + (off + (lane >> 3) * 8) * 2, boff, lo_off,
-                                min(8, (len + 15) / 16), nt);
+                                min(kSplitCols / 2, len), nt);
         __syncwarp();
         if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
         slot.next(t.stages);
@@ -683,9 +713,10 @@ layer_experts(Layer a) {
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int i = 0; i < kMaxStages; ++i) {
-      tma::mbar_init(&ring.full[i], kProducers * 32);
+      tma::mbar_init(&ring.full[i], kProducers);
       tma::mbar_init(&ring.empty[i], kConsumers);
     }
+    tma::mbar_init_fence();
   }
   make_tables(a, tb, kLayerThreads);
   const GiveUp g{&gave_up, a.err};
@@ -701,13 +732,14 @@ layer_experts(Layer a) {
     else produce<false, false>(a, tb, t, p1, ring, slot, unused, g, tid);
     if (fast2) produce<true, true>(a, tb, t, p2, ring, slot, unused, g, tid);
     else produce<true, false>(a, tb, t, p2, ring, slot, unused, g, tid);
-    cp_async_wait();
+    if (lane == 0) drain(t, ring, slot, unused, g);
     return;
   }
   int buffer = 0;
   const bool wide = t.rows == 64;
   if (wide) consume<D, true, false>(a, tb, t, p1, ring, slot, red, buffer, g);
   else consume<D, false, false>(a, tb, t, p1, ring, slot, red, buffer, g);
+  fence_async_proxy();                   // the activations are read by bulk copies
   consumers_sync();
   if (threadIdx.x == 0) grid_arrive(&a.barrier[0]);
   if (wide) consume<D, true, true>(a, tb, t, p2, ring, slot, red, buffer, g);
