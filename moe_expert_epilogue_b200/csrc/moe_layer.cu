@@ -15,19 +15,25 @@
 // The products.  A work item is a tile of weight rows of one unit (an expert and
 // up to 32 of its tokens); the weights are the 16-row operand of
 // mma.m16n8k16 and the tokens its 8 columns, so one pass over the weights serves
-// all of the unit's tokens.  Four producer warps copy 32 KB of weights at a time
-// and the tokens' matching columns into a ring of shared-memory stages (one
-// bulk copy a row); eight consumer warps multiply.  The producers run ahead of the
-// barrier between the products: the second product's first stages of weights are
-// fetched while the slowest CTA finishes the first.
+// all of the unit's tokens.  One producer warp brings 32 KB of weights at a time
+// into a ring of shared-memory stages by bulk copies, three others the tokens'
+// matching columns (cp.async); eight consumer warps multiply.  The weight
+// producer waits for nothing but free stages: while the slowest CTA finishes the
+// first product, the others' rings fill with the second's weights.
 //
 // The summation order is the same however a product is tiled: the axis is cut
 // into blocks of 256, block c's halves of 128 are accumulated in order into the
-// partial sums (c mod 4, half), and these eight are added in a fixed tree.  A
-// tile of 64 rows holds the four block classes in registers and lets four warps
-// share a block half; a tile of 16 rows gives each of the eight partial sums to
-// a warp.  The small tile is for few items: with 64-row tiles one token's 8 x 64
-// tiles leave a seventh of 148 CTAs idle in the last round.
+// partial sums (c mod 4, half), and these eight are added in a fixed tree.
+//   kWide   tiles of 64 rows by 256 columns: 2-D tensor copies of 64 columns
+//           (128-byte swizzle); four warps share a block half, each keeping the
+//           four block classes of its 16 rows in registers
+//   kNarrow tiles of 16 rows by 1024 columns, up to 8 tokens a unit: one bulk copy
+//           of 2 KB a row; each warp has one of the eight partial sums
+//   kAny    as kNarrow where rows start off 16-byte boundaries: the copies take
+//           the 16-byte words around a row, and the consumers shift
+// Row copies of 512 bytes instead of kWide's boxes were bound by their number:
+// halving their bytes changed nothing.
+#include <cuda.h>
 #include <math.h>
 
 #include <type_traits>
@@ -42,11 +48,12 @@ namespace moe {
 namespace {
 
 constexpr int kMaxTokens = 128, kMaxSlots = 1024, kMaxLayerExperts = 512;
-constexpr int kUnitTokens = 32;                        // tokens of one unit at most
-constexpr int kMaxUnits = kMaxLayerExperts + kMaxSlots / kUnitTokens;
+constexpr int kUnitTokens = 32;                        // tokens of one unit at most,
+constexpr int kNarrowTokens = 8;                       // or in tiles of 16 rows
+constexpr int kMaxUnits = kMaxLayerExperts + kMaxSlots / kNarrowTokens;
 constexpr int kBarriers = 2;
 
-// One expert and up to kUnitTokens of its tokens: a row of the product's work.
+// One expert and up to kUnitTokens (kNarrowTokens) of its tokens.
 struct Unit { uint16_t expert, first, count; };
 
 // The choice, as every CTA holds it: slots are (token, k) pairs, token-major;
@@ -77,7 +84,7 @@ struct Layer {
   int tokens, hidden, inter, E, K;
   int64_t ld_x, ld_logits, ld_shared, ld_residual, ld_out;
   int logits_dt;
-  bool router_f32, softmax, normalise, aligned_x, aligned_w1, aligned_w2;
+  bool router_f32, softmax, normalise;
   float scale, limit;
   int32_t* err;
   // workspace
@@ -161,8 +168,9 @@ __device__ void choose_token(const Layer& a, Tables& tb, int t, int lane) {
   if (lane == 0) tb.live[t] = (uint8_t)__popc(live);
 }
 
-// Fills the tables; all `threads` threads of the CTA take part.
-__device__ void make_tables(const Layer& a, Tables& tb, int threads) {
+// Fills the tables, units of at most `unit_tokens`; all `threads` threads of the
+// CTA take part.
+__device__ void make_tables(const Layer& a, Tables& tb, int unit_tokens, int threads) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int live = (int)live_tokens(a.valid, a.tokens, a.err);
   for (int e = threadIdx.x; e < a.E; e += threads) tb.count[e] = 0;
@@ -191,8 +199,8 @@ __device__ void make_tables(const Layer& a, Tables& tb, int threads) {
     int base = 0, units = 0, most = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane, n = e < a.E ? tb.count[e] : 0;
-      const int u = (n + kUnitTokens - 1) / kUnitTokens;
-      most = max(most, min(n, kUnitTokens));
+      const int u = (n + unit_tokens - 1) / unit_tokens;
+      most = max(most, min(n, unit_tokens));
       int sn = n, su = u;                                   // inclusive prefix sums
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -203,8 +211,8 @@ __device__ void make_tables(const Layer& a, Tables& tb, int threads) {
         const int first = base + sn - n;
         tb.first[e] = (uint16_t)first;
         for (int i = 0; i < u; ++i)
-          tb.unit[units + su - u + i] = {(uint16_t)e, (uint16_t)(first + i * kUnitTokens),
-                                         (uint16_t)min(kUnitTokens, n - i * kUnitTokens)};
+          tb.unit[units + su - u + i] = {(uint16_t)e, (uint16_t)(first + i * unit_tokens),
+                                         (uint16_t)min(unit_tokens, n - i * unit_tokens)};
       }
       base += __shfl_sync(kAll, sn, 31);
       units += __shfl_sync(kAll, su, 31);
@@ -297,51 +305,49 @@ __device__ __forceinline__ float ld_cg(const float* p) {
   return v;
 }
 
-constexpr int kConsumers = 8, kProducers = 4;                    // warps
-constexpr int kLayerThreads = (kConsumers + kProducers) * 32;
+constexpr int kConsumers = 8, kTokenWarps = 3;                   // and one weight warp
+constexpr int kLayerThreads = (kConsumers + 1 + kTokenWarps) * 32;
 constexpr int kSplitCols = 256;                                  // a block of the axis
 constexpr int kMaxStages = 8;
 constexpr int kRedBytes = 4 * 4 * 32 * 16;                       // one buffer of partial sums
 
-// A tile's shape: 64 rows by 256 columns or 16 by 1024 (32 KB of weights).
+enum Tiling { kWide, kNarrow, kAny };
+
+template <Tiling T>
 struct Tile {
-  int rows, cols, pitch, a_bytes, stage_bytes, stages;
+  static constexpr int kRows = T == kWide ? 64 : 16;
+  static constexpr int kCols = T == kWide ? kSplitCols : 4 * kSplitCols;
+  // rows of an odd multiple of 16 bytes: ldmatrix without bank conflicts
+  static constexpr int kTokenPitch = kCols * 2 + 16;
+  static constexpr int kPitch = T == kAny ? kCols * 2 + 32 : kCols * 2 + 16;   // not of kWide
+  static constexpr int kWeightBytes = T == kWide ? kRows * kCols * 2 : kRows * kPitch;
+  static constexpr int kTokens = T == kWide ? kUnitTokens : kNarrowTokens;
 };
 
-constexpr int kRingBytes = (232448 - (int)sizeof(Tables) - 2 * kRedBytes - 256) / 128 * 128;
-
-__device__ __forceinline__ Tile tile_shape(const Layer& a, const Tables& tb) {
-  Tile t;
-  const int tiles64 = (2 * a.inter + 63) / 64;
-  const bool wide = tb.most > 8 || (int64_t)tb.units * tiles64 >= 8 * (int64_t)gridDim.x;
-  t.rows = wide ? 64 : 16;
-  t.cols = wide ? kSplitCols : 4 * kSplitCols;
-  t.pitch = t.cols * 2 + 16;          // an odd multiple of 16 bytes: ldmatrix without conflicts
-  t.a_bytes = t.rows * t.pitch;
-  t.stage_bytes = t.a_bytes + 2 * tb.most * t.pitch;
-  t.stages = min(kMaxStages, kRingBytes / t.stage_bytes);
-  return t;
-}
+// The ring: stages of weights, then up to 2 * most token rows.
+constexpr int kRingBytes = (232448 - (int)sizeof(Tables) - 2 * kRedBytes - 256) / 1024 * 1024 - 1024;
+static_assert(kRingBytes / 1024 >= 2 * (32 + 2 * kUnitTokens * (kSplitCols * 2 + 16) / 1024 + 1),
+              "two stages at least");
 
 struct Ring {
-  uint8_t* base;
+  uint8_t* base;         // 1024-byte aligned
   uint64_t *full, *empty;
+  int stage_bytes, stages;
 };
 
 // A place in the ring: the slot and the parity of its current use.
 struct Slot {
-  int at;
-  uint32_t parity;
-  __device__ __forceinline__ void next(int stages) {
-    if (++at == stages) { at = 0; parity ^= 1u; }
+  int at = 0;
+  uint32_t parity = 0;
+  int fresh;             // slots not used yet
+  __device__ explicit Slot(const Ring& r) : fresh(r.stages) {}
+  __device__ __forceinline__ void next(const Ring& r) {
+    if (++at == r.stages) { at = 0; parity ^= 1u; }
   }
-};
-
-// The stages of one CTA's items of a product, in order.
-struct Walk {
-  int item, chunk;
-  __device__ __forceinline__ void next(int chunks) {
-    if (++chunk == chunks) { chunk = 0; item += gridDim.x; }
+  // Waits until the slot may be overwritten.
+  __device__ __forceinline__ void claim(const Ring& r, const GiveUp& g) {
+    if (fresh > 0) --fresh;
+    else wait_phase(&r.empty[at], parity ^ 1u, g);
   }
 };
 
@@ -349,56 +355,152 @@ struct Product {
   int axis;      // columns of the weights
   int tiles;     // row tiles of an expert
   int items;     // units x tiles
-  int chunks;    // stages per item
+  int chunks;    // stages per item; an empty axis has one empty stage
 };
 
-__device__ __forceinline__ Product make_product(const Layer& a, const Tables& tb, const Tile& t,
-                                                bool second) {
+template <Tiling T, bool SECOND>
+__device__ __forceinline__ Product make_product(const Layer& a, const Tables& tb) {
+  using S = Tile<T>;
   Product p;
-  p.axis = second ? a.inter : a.hidden;
-  p.tiles = second ? (a.hidden + t.rows - 1) / t.rows : (2 * a.inter + t.rows - 1) / t.rows;
+  p.axis = SECOND ? a.inter : a.hidden;
+  p.tiles = ((SECOND ? a.hidden : 2 * a.inter) + S::kRows - 1) / S::kRows;
+  if (!SECOND) p.tiles = (a.inter + S::kRows / 2 - 1) / (S::kRows / 2);
   p.items = tb.units * p.tiles;
-  p.chunks = max(1, (p.axis + t.cols - 1) / t.cols);   // an empty axis: one empty stage, sums of 0
+  p.chunks = max(1, (p.axis + S::kCols - 1) / S::kCols);
   return p;
+}
+
+// Calls f(unit, tile, first column, columns) for each stage of this CTA's items,
+// in order.
+template <Tiling T, class F>
+__device__ __forceinline__ void for_stages(const Tables& tb, const Product& p, F f) {
+  for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    const Unit u = tb.unit[item / p.tiles];
+    const int tile = item % p.tiles;
+    for (int c = 0; c < p.chunks; ++c) {
+      const int k0 = c * Tile<T>::kCols;
+      f(u, tile, k0, min(Tile<T>::kCols, p.axis - k0));
+    }
+  }
 }
 
 // ---- producers
 
-// Rows of a stage: the tile's weight rows, then the unit's token rows (of the
-// second product: both halves of their activations).  At most 64 + 2 * 32: each
-// producer thread owns one of them and copies its columns with one bulk copy,
-// where rows start on 16-byte boundaries (FAST); other weights are put together
-// element by element by all producers.
+struct WeightMaps {
+  CUtensorMap w1, w2;    // kWide
+};
 
-// Weight row r of an item, or null past the last.  First product: a tile's
-// 16-row groups hold 8 gate rows and the 8 up rows of the same columns of the
-// activation.
-template <bool SECOND>
-__device__ __forceinline__ const uint16_t* weight_row(const Layer& a, const Tile& t, const Unit& u,
-                                                      int tile, int r) {
-  if (SECOND) {
-    const int col = tile * t.rows + r;
-    if (col >= a.hidden) return nullptr;
-    return static_cast<const uint16_t*>(a.w2) + ((int64_t)u.expert * a.hidden + col) * a.inter;
-  }
-  const int j = tile * (t.rows / 2) + (r >> 4) * 8 + (r & 7);
-  if (j >= a.inter) return nullptr;
-  return static_cast<const uint16_t*>(a.w1) +
-         (((int64_t)u.expert * 2 + ((r >> 3) & 1)) * a.inter + j) * a.hidden;
+// Box of 64 columns of a 3-D tensor into shared memory (128-byte swizzle).
+__device__ __forceinline__ void tensor_load(void* dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tma::smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(tma::smem_addr(bar))
+      : "memory");
 }
 
+// Weight row r of a 16-row tile, or null past the last.  First product: 8 gate
+// rows, then the 8 up rows of the same columns of the activation.
 template <bool SECOND>
-__device__ __forceinline__ const uint16_t* token_row(const Layer& a, const Tables& tb,
-                                                     const Unit& u, int r) {
+__device__ __forceinline__ const uint16_t* weight_row(const Layer& a, int expert, int tile,
+                                                      int r) {
   if (SECOND) {
-    const int n = r < u.count ? r : r - u.count;
-    return a.h + ((int64_t)(u.first + n) * 2 + (r < u.count ? 0 : 1)) * a.ld_h;
+    const int col = tile * 16 + r;
+    if (col >= a.hidden) return nullptr;
+    return static_cast<const uint16_t*>(a.w2) + ((int64_t)expert * a.hidden + col) * a.inter;
   }
-  return static_cast<const uint16_t*>(a.x) + tb.token[u.first + r] * a.ld_x;
+  const int j = tile * 8 + (r & 7);
+  if (j >= a.inter) return nullptr;
+  return static_cast<const uint16_t*>(a.w1) +
+         (((int64_t)expert * 2 + (r >> 3)) * a.inter + j) * a.hidden;
+}
+
+template <Tiling T, bool SECOND>
+__device__ __forceinline__ void produce_weights(const Layer& a, const WeightMaps& maps,
+                                                const Tables& tb, const Ring& ring, Slot& slot,
+                                                const GiveUp& g, int lane) {
+  using S = Tile<T>;
+  for_stages<T>(tb, make_product<T, SECOND>(a, tb), [&](Unit u, int tile, int k0, int len) {
+    slot.claim(ring, g);
+    uint8_t* stage = ring.base + (size_t)slot.at * ring.stage_bytes;
+    uint64_t* full = &ring.full[slot.at];
+    if (T == kWide) {
+      // 64-column boxes of 64 rows (first product: 32 gate rows, 32 up rows)
+      const int boxes = (len + 63) / 64;
+      if (lane == 0) {
+        tma::mbar_arrive_expect_tx(full, boxes * 8192);
+        for (int b = 0; b < boxes; ++b) {
+          if (SECOND) {
+            tensor_load(stage + b * 8192, &maps.w2, k0 + b * 64, tile * 64, u.expert, full);
+          } else {
+            tensor_load(stage + b * 8192, &maps.w1, k0 + b * 64, tile * 32, u.expert * 2, full);
+            tensor_load(stage + b * 8192 + 4096, &maps.w1, k0 + b * 64, tile * 32,
+                        u.expert * 2 + 1, full);
+          }
+        }
+      }
+    } else {
+      const uint16_t* src = lane < 16 ? weight_row<SECOND>(a, u.expert, tile, lane) : nullptr;
+      uint8_t* dst = stage + lane * S::kPitch;
+      uint32_t bytes = src ? len * 2 : 0;
+      if (src) src += k0;
+      if (T == kAny) {
+        // the 16-byte words that hold the row, unless they reach past the tensor
+        // (its first and its last row): those are put together element by element
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(SECOND ? a.w2 : a.w1);
+        const uintptr_t hi = lo + (uintptr_t)2 * a.E * (SECOND ? 1 : 2) * a.hidden * a.inter;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15;
+        const uintptr_t to = (reinterpret_cast<uintptr_t>(src) + bytes + 15) & ~(uintptr_t)15;
+        unsigned edge = __ballot_sync(kAll, bytes > 0 && (from < lo || to > hi));
+        const int shift = (int)(reinterpret_cast<uintptr_t>(src) - from);
+        for (unsigned rows = edge; rows; rows &= rows - 1) {
+          const int r = __ffs(rows) - 1;
+          const auto* row = reinterpret_cast<const uint16_t*>(
+              __shfl_sync(kAll, reinterpret_cast<uint64_t>(src), r));
+          auto* to_row = reinterpret_cast<uint16_t*>(stage + r * S::kPitch +
+                                                     __shfl_sync(kAll, shift, r));
+          for (int c = lane; c < len; c += 32) to_row[c] = __ldg(row + c);
+        }
+        if (edge) fence_async_proxy();   // later bulk copies into the stage come after
+        __syncwarp();
+        if (edge >> lane & 1) bytes = 0;
+        if (bytes > 0) {
+          src = reinterpret_cast<const uint16_t*>(from);
+          bytes = (uint32_t)(to - from);
+        }
+      }
+      const uint32_t total = __reduce_add_sync(kAll, bytes);
+      if (lane == 0) tma::mbar_arrive_expect_tx(full, total);
+      __syncwarp();
+      if (bytes > 0) tma::bulk_load(dst, src, bytes, full);
+    }
+    slot.next(ring);
+  });
+}
+
+// Waits until every stage filled has landed: a CTA does not end before its copies.
+__device__ __forceinline__ void drain(const Ring& ring, const Slot& slot, const GiveUp& g) {
+  for (int i = 0; i < ring.stages - slot.fresh; ++i) {
+    const uint32_t parity = i < slot.at ? slot.parity : slot.parity ^ 1u;
+    if (!tma::mbar_wait(&ring.full[i], parity)) flag_error(g.err, MOE_DEVERR_TIMEOUT);
+  }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival of this thread once all of its cp.async have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tma::smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Columns [col, col + 8) of a row of `len` columns into shared memory, zeros
-// past the end.
+// past the end, element by element.
 __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, int col, int len) {
   uint32_t w[4];
 #pragma unroll
@@ -413,111 +515,36 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, int col
                : "memory");
 }
 
-// `rows` rows of a stage element by element; row(r) is a row's start at this
-// stage's first column, or null.
-template <class Row>
-__device__ __forceinline__ void copy_rows(uint32_t dst, int rows, int pitch, int len, int tid,
-                                          Row row) {
-  const int pieces = (len + 7) / 8;
-  for (int r = tid >> 5; r < rows; r += kProducers) {
-    const uint16_t* src = row(r);
-    if (!src) continue;
+// The stages' columns of the unit's tokens (second product: of both halves of
+// their activations), zeros up to a multiple of 8.
+template <Tiling T, bool SECOND>
+__device__ __forceinline__ void produce_tokens(const Layer& a, const Tables& tb, const Ring& ring,
+                                               Slot& slot, const GiveUp& g, int warp, int lane) {
+  using S = Tile<T>;
+  for_stages<T>(tb, make_product<T, SECOND>(a, tb), [&](Unit u, int, int k0, int len) {
+    slot.claim(ring, g);
+    const uint32_t dst = tma::smem_addr(ring.base + (size_t)slot.at * ring.stage_bytes) +
+                         S::kWeightBytes;
+    const int rows = SECOND ? 2 * u.count : u.count, pieces = (len + 7) / 8;
+    for (int r = warp; r < rows; r += kTokenWarps) {
+      const uint16_t* src;
+      if (SECOND) {
+        const int n = r < u.count ? r : r - u.count;
+        src = a.h + ((int64_t)(u.first + n) * 2 + (r < u.count ? 0 : 1)) * a.ld_h + k0;
+      } else {
+        src = static_cast<const uint16_t*>(a.x) + tb.token[u.first + r] * a.ld_x + k0;
+      }
 #pragma unroll 4
-    for (int c = tid & 31; c < pieces; c += 32) copy8(dst + r * pitch + c * 16, src, c * 8, len);
-  }
-}
-
-template <bool SECOND, bool FAST>
-__device__ __forceinline__ void produce(const Layer& a, const Tables& tb, const Tile& t,
-                                        const Product& p, const Ring& ring, Slot& slot,
-                                        int& unused, const GiveUp& g, int tid) {
-  constexpr bool kFastTokens = SECOND || FAST;   // the workspace's rows are aligned
-  const int lane = tid & 31;
-  // This thread's row of the item, if it copies one.
-  struct Mine { const uint16_t* src; bool weights; };
-  auto mine = [&](int item) {
-    const Unit u = tb.unit[item / p.tiles];
-    Mine m{nullptr, tid < t.rows};
-    if (m.weights) {
-      if (FAST) m.src = weight_row<SECOND>(a, t, u, item % p.tiles, tid);
-    } else if (kFastTokens && tid - t.rows < (SECOND ? 2 : 1) * u.count) {
-      m.src = token_row<SECOND>(a, tb, u, tid - t.rows);
+      for (int c = lane; c < pieces; c += 32) {
+        // (the activation's rows end with zeros up to a multiple of 8)
+        if (SECOND || T != kAny) cp_async16(dst + r * S::kTokenPitch + c * 16, src + c * 8);
+        else copy8(dst + r * S::kTokenPitch + c * 16, src, c * 8, len);
+      }
     }
-    return m;
-  };
-  auto claim = [&] {                     // wait until the slot may be overwritten
-    if (unused > 0) --unused;
-    else wait_phase(&ring.empty[slot.at], slot.parity ^ 1u, g);
-  };
-  // Parts of one stage: copies of weights and / or tokens; `last`: this warp's
-  // arrival, with which the copies announced complete the stage.
-  auto fill = [&](const Walk& w, const Mine& m, int at, bool weights, bool tokens, bool last) {
-    const int k0 = w.chunk * t.cols, len = min(t.cols, p.axis - k0);
-    uint8_t* stage = ring.base + (size_t)at * t.stage_bytes;
-    if (!FAST && weights) {
-      const Unit u = tb.unit[w.item / p.tiles];
-      copy_rows(tma::smem_addr(stage), t.rows, t.pitch, len, tid, [&](int r) {
-        const uint16_t* row = weight_row<SECOND>(a, t, u, w.item % p.tiles, r);
-        return row ? row + k0 : nullptr;
-      });
-      if (!kFastTokens)
-        copy_rows(tma::smem_addr(stage + t.a_bytes), u.count, t.pitch, len, tid,
-                  [&](int r) { return token_row<SECOND>(a, tb, u, r) + k0; });
-      fence_async_proxy();               // later bulk copies into the stage come after
-      __syncwarp();
-    }
-    const bool copies = m.src && len > 0 && (m.weights ? weights : tokens);
-    const uint32_t bytes = SECOND && !FAST ? (len + 7) / 8 * 16 : len * 2;
-    const uint32_t total = __popc(__ballot_sync(kAll, copies)) * bytes;
-    if (lane == 0) {
-      if (last) tma::mbar_arrive_expect_tx(&ring.full[at], total);
-      else if (total) tma::mbar_expect_tx(&ring.full[at], total);
-    }
-    __syncwarp();
-    if (copies) tma::bulk_load(stage + tid * t.pitch, m.src + k0, bytes, &ring.full[at]);
-  };
-  Walk w{(int)blockIdx.x, 0};
-  Mine m{};
-  if (SECOND) {
-    // weights ahead of the barrier, then the activations they meet
-    Walk ahead = w;
-    Slot first = slot;
-    int n = 0;
-    for (; n < t.stages && ahead.item < p.items; ++n) {
-      if (ahead.chunk == 0) m = mine(ahead.item);
-      claim();
-      fill(ahead, m, slot.at, true, false, false);
-      ahead.next(p.chunks);
-      slot.next(t.stages);
-    }
-    if (lane == 0) grid_wait(&a.barrier[0], g);
-    __syncwarp();
-    fence_async_proxy();                 // the activations are read by bulk copies
-    for (; n > 0; --n) {
-      if (w.chunk == 0) m = mine(w.item);
-      fill(w, m, first.at, false, true, true);
-      w.next(p.chunks);
-      first.next(t.stages);
-    }
-    if (w.item < p.items) m = mine(w.item);
-  }
-  while (w.item < p.items) {
-    if (w.chunk == 0) m = mine(w.item);
-    claim();
-    fill(w, m, slot.at, true, true, true);
-    w.next(p.chunks);
-    slot.next(t.stages);
-  }
-}
-
-// Waits until every stage filled has landed: a CTA does not end before its copies.
-__device__ __forceinline__ void drain(const Tile& t, const Ring& ring, const Slot& slot, int unused,
-                                      const GiveUp& g) {
-  for (int i = 0; i < t.stages; ++i) {
-    if (unused > 0 && i >= t.stages - unused) continue;
-    const uint32_t parity = i < slot.at ? slot.parity : slot.parity ^ 1u;
-    if (!tma::mbar_wait(&ring.full[i], parity)) flag_error(g.err, MOE_DEVERR_TIMEOUT);
-  }
+    if (SECOND || T != kAny) cp_async_arrive(&ring.full[slot.at]);
+    else tma::mbar_arrive(&ring.full[slot.at]);
+    slot.next(ring);
+  });
 }
 
 // ---- consumers
@@ -544,36 +571,72 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Two neighbouring 16-bit elements at any even address of shared memory, the
+// second (both) cleared where fewer than two (one) are left.
+__device__ __forceinline__ uint32_t lds_pair(uint32_t addr, int left) {
+  uint32_t w0, w1;
+  const uint32_t at = addr & ~3u;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at));
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"(at + 4));
+  const uint32_t v = __funnelshift_r(w0, w1, (addr & 2u) * 8);
+  return left >= 2 ? v : left == 1 ? v & 0xffffu : 0u;
+}
+
+// Where a warp's 16 rows of weights lie in a stage.
+template <Tiling T>
+struct WeightAddr {
+  uint32_t row;           // kWide, kNarrow: this lane's ldmatrix row; kAny: row g
+  uint32_t row8;          // kAny: row g + 8
+};
+
+// The fragment of k-step ks (16 columns) of this warp's 128.
+template <Tiling T>
+__device__ __forceinline__ void load_weights(uint32_t (&r)[4], const WeightAddr<T>& w, int half,
+                                             int ks, int lane, int len) {
+  if constexpr (T == kWide) {
+    const int piece = (ks & 3) * 2 + (lane >> 4);
+    ldsm4(r, w.row + (half * 2 + (ks >> 2)) * 8192 + ((piece ^ (lane & 7)) * 16));
+  } else if constexpr (T == kNarrow) {
+    ldsm4(r, w.row + ks * 32);
+  } else {
+    const int c = ks * 16 + (lane & 3) * 2;
+    r[0] = lds_pair(w.row + c * 2, len - c);
+    r[1] = lds_pair(w.row8 + c * 2, len - c);
+    r[2] = lds_pair(w.row + c * 2 + 16, len - c - 8);
+    r[3] = lds_pair(w.row8 + c * 2 + 16, len - c - 8);
+  }
+}
+
 // This warp's `len` (up to 128) columns of one stage: acc[j] += weights (16
 // rows) x tokens 8 j .. 8 j + 7.  Columns past the unit's last token repeat it;
-// nothing reads their sums.  The axis ends on a multiple of 8 columns: of a last
-// k-step of 16 with 8, the upper half of the fragments is cleared, since what
-// lies there in shared memory may be anything.
-template <class D, bool SECOND, int NT>
-__device__ __forceinline__ void multiply(float (&acc)[NT][4], uint32_t wrow, uint32_t trow,
-                                         const uint32_t (&boff)[NT], uint32_t lo_off, int len,
-                                         int nt) {
+// nothing reads their sums.  Shared memory is filled to a multiple of 8 columns:
+// of a last k-step of 16 with 8, the upper half of the fragments is cleared,
+// since what lies there may be anything.
+template <class D, Tiling T, bool SECOND, int NT>
+__device__ __forceinline__ void multiply(float (&acc)[NT][4], const WeightAddr<T>& w,
+                                         uint32_t tokens, const uint32_t (&boff)[NT],
+                                         uint32_t lo_off, int len, int nt, int half, int lane) {
 #pragma unroll
   for (int kp = 0; kp < 4; ++kp) {
     if (kp * 32 >= len) break;
     uint32_t a0[4], a1[4];
-    ldsm4(a0, wrow + kp * 64);
-    ldsm4(a1, wrow + kp * 64 + 32);       // (within the stage, unused past the last k-step)
     const bool both = kp * 32 + 16 < len;
     const bool cut0 = kp * 32 + 8 >= len, cut1 = kp * 32 + 24 >= len;
+    load_weights<T>(a0, w, half, 2 * kp, lane, len);
+    if (both) load_weights<T>(a1, w, half, 2 * kp + 1, lane, len);
     if (cut0) a0[2] = a0[3] = 0;
     if (cut1) a1[2] = a1[3] = 0;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
       uint32_t b[4];
-      ldsm4(b, trow + boff[j] + kp * 64);
+      ldsm4(b, tokens + boff[j] + kp * 64);
       if (cut0) b[1] = 0;
       if (cut1) b[3] = 0;
       mma16816<D>(acc[j], a0, b[0], b[1]);
       if (SECOND) {
         uint32_t l[4];
-        ldsm4(l, trow + boff[j] + lo_off + kp * 64);
+        ldsm4(l, tokens + boff[j] + lo_off + kp * 64);
         if (cut0) l[1] = 0;
         if (cut1) l[3] = 0;
         mma16816<D>(acc[j], a0, l[0], l[1]);
@@ -589,6 +652,7 @@ __device__ __forceinline__ void multiply(float (&acc)[NT][4], uint32_t wrow, uin
 }
 
 // Lane (g, q) of a 16 x 8 block of sums: rows g, g + 8, tokens 2 q, 2 q + 1.
+// `row0`: hidden column (second product) or activation column of row 0.
 template <class D, bool SECOND>
 __device__ __forceinline__ void finish(const Layer& a, const Tables& tb, const Unit& u, int row0,
                                        int tok0, int lane, const float (&c)[4]) {
@@ -603,7 +667,7 @@ __device__ __forceinline__ void finish(const Layer& a, const Tables& tb, const U
       if (row0 + g < a.hidden) y[row0 + g] = c[i];
       if (row0 + g + 8 < a.hidden) y[row0 + g + 8] = c[i + 2];
     } else {
-      const int j = row0 / 2 + g;
+      const int j = row0 + g;
       uint16_t* h = a.h + (int64_t)pos * 2 * a.ld_h + j;
       if (j < a.inter)
         split<D>(activation(c[i], c[i + 2], tb.weight[tb.order[pos]], a.limit), h, h + a.ld_h);
@@ -617,52 +681,69 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-template <class D, bool WIDE, bool SECOND>
-__device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const Tile& t,
-                                        const Product& p, const Ring& ring, Slot& slot,
-                                        float4* red, int& buffer, const GiveUp& g) {
+template <class D, Tiling T, bool SECOND>
+__device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const Ring& ring,
+                                        Slot& slot, float4* red, int& buffer, const GiveUp& g) {
+  using S = Tile<T>;
+  constexpr bool WIDE = T == kWide;
   constexpr int NS = WIDE ? 4 : 1, NT = WIDE ? 4 : 1;
+  const Product p = make_product<T, SECOND>(a, tb);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = warp >> 2, quarter = warp & 3;
   const int group = WIDE ? quarter : 0;                       // 16-row group of the tile
   const int off = (WIDE ? 0 : quarter * kSplitCols) + half * (kSplitCols / 2);
   const uint32_t ring_base = tma::smem_addr(ring.base);
-  const uint32_t wlane = (group * 16 + (lane & 15)) * t.pitch + (off + (lane >> 4) * 8) * 2;
   for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
     const Unit u = tb.unit[item / p.tiles];
+    const int tile = item % p.tiles;
     const int nt = (u.count + 7) / 8;
     uint32_t boff[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) boff[j] = min(j * 8 + (lane & 7), u.count - 1) * t.pitch;
-    const uint32_t lo_off = u.count * t.pitch;
+    for (int j = 0; j < NT; ++j) boff[j] = min(j * 8 + (lane & 7), u.count - 1) * S::kTokenPitch;
+    const uint32_t lo_off = u.count * S::kTokenPitch;
+    WeightAddr<T> rel;                                        // within the stage
+    if (T == kWide) {
+      // gate rows 0 .. 31 and up rows 32 .. 63 of the first product's boxes
+      rel.row = (SECOND ? group * 16 + (lane & 15)
+                        : group * 8 + (lane & 7) + (lane & 8) * 4) * 128;
+    } else if (T == kNarrow) {
+      rel.row = (lane & 15) * S::kPitch + (off + (lane >> 4) * 8) * 2;
+    } else {
+      const int r = lane >> 2;
+      const auto lo = reinterpret_cast<uintptr_t>(weight_row<SECOND>(a, u.expert, tile, r));
+      const auto hi = reinterpret_cast<uintptr_t>(weight_row<SECOND>(a, u.expert, tile, r + 8));
+      rel.row = r * S::kPitch + off * 2 + (uint32_t)(lo & 15);
+      rel.row8 = (r + 8) * S::kPitch + off * 2 + (uint32_t)(hi & 15);
+    }
     float acc[NS][NT][4] = {};
     for (int c0 = 0; c0 < p.chunks; c0 += NS) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         if (c0 + s >= p.chunks) break;
-        const int len = min(t.cols, p.axis - (c0 + s) * t.cols) - off;
-        const uint32_t stage = ring_base + slot.at * t.stage_bytes;
+        const int len = min(S::kCols, p.axis - (c0 + s) * S::kCols) - off;
+        const uint32_t stage = ring_base + slot.at * ring.stage_bytes;
         wait_phase(&ring.full[slot.at], slot.parity, g);
         __syncwarp();
-        multiply<D, SECOND, NT>(acc[s], stage + wlane,
-                                stage + t.a_bytes + (off + (lane >> 3) * 8) * 2, boff, lo_off,
-                                min(kSplitCols / 2, len), nt);
+        WeightAddr<T> w = rel;
+        w.row += stage;
+        w.row8 += stage;
+        multiply<D, T, SECOND, NT>(acc[s], w,
+                                   stage + S::kWeightBytes + (off + (lane >> 3) * 8) * 2, boff,
+                                   lo_off, min(kSplitCols / 2, len), nt, half, lane);
         __syncwarp();
         if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
-        slot.next(t.stages);
+        slot.next(ring);
       }
     }
     // the eight partial sums, in one order: ((0 + 1) + (2 + 3)) of each half, then the halves
     float4* r = red + buffer * (kRedBytes / 16);
-    const int row0 = (item % p.tiles) * t.rows;
-    if (WIDE) {
+    if constexpr (WIDE) {
       float sum[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sum[j][i] = (acc[0][j][i] + acc[NS > 1 ? 1 : 0][j][i]) +
-                      (acc[NS > 2 ? 2 : 0][j][i] + acc[NS > 3 ? 3 : 0][j][i]);
+          sum[j][i] = (acc[0][j][i] + acc[1][j][i]) + (acc[2][j][i] + acc[3][j][i]);
         if (half == 1 && j < nt)
           r[(group * 4 + j) * 32 + lane] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
       }
@@ -673,7 +754,8 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
           if (j >= nt) break;
           const float4 o = r[(group * 4 + j) * 32 + lane];
           const float c[4] = {sum[j][0] + o.x, sum[j][1] + o.y, sum[j][2] + o.z, sum[j][3] + o.w};
-          finish<D, SECOND>(a, tb, u, row0 + group * 16, j * 8, lane, c);
+          finish<D, SECOND>(a, tb, u, SECOND ? tile * 64 + group * 16 : tile * 32 + group * 8,
+                            j * 8, lane, c);
         }
       }
     } else {
@@ -693,57 +775,60 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
         }
         const float s[4] = {c[0][0] + c[1][0], c[0][1] + c[1][1], c[0][2] + c[1][2],
                             c[0][3] + c[1][3]};
-        finish<D, SECOND>(a, tb, u, row0, 0, lane, s);
+        finish<D, SECOND>(a, tb, u, SECOND ? tile * 16 : tile * 8, 0, lane, s);
       }
     }
     buffer ^= 1;      // the next item's sums must not meet readers of these
   }
 }
 
-template <class D>
+template <class D, Tiling T>
 __global__ void __launch_bounds__(kLayerThreads, 1)
-layer_experts(Layer a) {
+layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMaps maps) {
+  using S = Tile<T>;
   __shared__ Tables tb;
   __shared__ float4 red[2 * kRedBytes / 16];
   __shared__ uint64_t bars[2 * kMaxStages];
   __shared__ int gave_up;
-  extern __shared__ __align__(128) uint8_t ring_mem[];
+  extern __shared__ uint8_t ring_mem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Ring ring{ring_mem, bars, bars + kMaxStages};
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int i = 0; i < kMaxStages; ++i) {
-      tma::mbar_init(&ring.full[i], kProducers);
-      tma::mbar_init(&ring.empty[i], kConsumers);
+      tma::mbar_init(&bars[i], 1 + kTokenWarps * 32);
+      tma::mbar_init(&bars[kMaxStages + i], kConsumers);
     }
     tma::mbar_init_fence();
   }
-  make_tables(a, tb, kLayerThreads);
+  make_tables(a, tb, S::kTokens, kLayerThreads);
   const GiveUp g{&gave_up, a.err};
-  const Tile t = tile_shape(a, tb);
-  const Product p1 = make_product(a, tb, t, false), p2 = make_product(a, tb, t, true);
-  Slot slot{0, 0};
-  if (warp >= kConsumers) {
-    const int tid = threadIdx.x - kConsumers * 32;
-    int unused = t.stages;
-    const bool fast1 = a.hidden % 8 == 0 && a.ld_x % 8 == 0 && a.aligned_x && a.aligned_w1;
-    const bool fast2 = a.inter % 8 == 0 && a.aligned_w2;
-    if (fast1) produce<false, true>(a, tb, t, p1, ring, slot, unused, g, tid);
-    else produce<false, false>(a, tb, t, p1, ring, slot, unused, g, tid);
-    if (fast2) produce<true, true>(a, tb, t, p2, ring, slot, unused, g, tid);
-    else produce<true, false>(a, tb, t, p2, ring, slot, unused, g, tid);
-    if (lane == 0) drain(t, ring, slot, unused, g);
+  Ring ring;
+  ring.base = ring_mem + ((1024u - (tma::smem_addr(ring_mem) & 1023u)) & 1023u);
+  ring.full = bars;
+  ring.empty = bars + kMaxStages;
+  ring.stage_bytes = (S::kWeightBytes + 2 * tb.most * S::kTokenPitch + 1023) / 1024 * 1024;
+  ring.stages = min(kMaxStages, kRingBytes / ring.stage_bytes);
+  Slot slot(ring);
+  if (warp == kConsumers) {
+    produce_weights<T, false>(a, maps, tb, ring, slot, g, lane);
+    produce_weights<T, true>(a, maps, tb, ring, slot, g, lane);
+    if (lane == 0) drain(ring, slot, g);
+    return;
+  }
+  if (warp > kConsumers) {
+    const int w = warp - kConsumers - 1;
+    produce_tokens<T, false>(a, tb, ring, slot, g, w, lane);
+    if (lane == 0) grid_wait(&a.barrier[0], g);
+    __syncwarp();
+    produce_tokens<T, true>(a, tb, ring, slot, g, w, lane);
+    cp_async_wait();
     return;
   }
   int buffer = 0;
-  const bool wide = t.rows == 64;
-  if (wide) consume<D, true, false>(a, tb, t, p1, ring, slot, red, buffer, g);
-  else consume<D, false, false>(a, tb, t, p1, ring, slot, red, buffer, g);
-  fence_async_proxy();                   // the activations are read by bulk copies
+  consume<D, T, false>(a, tb, ring, slot, red, buffer, g);
   consumers_sync();
   if (threadIdx.x == 0) grid_arrive(&a.barrier[0]);
-  if (wide) consume<D, true, true>(a, tb, t, p2, ring, slot, red, buffer, g);
-  else consume<D, false, true>(a, tb, t, p2, ring, slot, red, buffer, g);
+  consume<D, T, true>(a, tb, ring, slot, red, buffer, g);
   consumers_sync();
   if (threadIdx.x == 0) {
     grid_arrive(&a.barrier[1]);
@@ -785,8 +870,60 @@ Space layer_space(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int6
   return s;
 }
 
+// The driver's tensor-map encoder, looked up once.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                           cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Boxes of 64 columns and `box` rows of a [depth, rows, cols] tensor of 16-bit
+// elements (only their bits are moved); outside of it they read zeros.
+int weight_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t depth,
+               int box) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return cuda_fail(cudaErrorNotSupported);
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1}, steps[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims,
+                            strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+template <class D, Tiling T>
+int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t stream) {
+  constexpr size_t smem = kRingBytes + 1024;
+  if (int rc = ensure_smem_limit((const void*)layer_experts<D, T>, smem)) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kLayerThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  (void)cudaLaunchKernelEx(&cfg, layer_experts<D, T>, a, maps);
+  return check_launch();
+}
+
 template <class D>
-int launch(Layer& a, cudaStream_t stream) {
+int launch(const Layer& a, cudaStream_t stream) {
   const dim3 grid = a.router_w ? dim3((unsigned)a.E, (unsigned)((a.tokens + kLogitTokens - 1) /
                                                                 kLogitTokens))
                                : dim3(1);
@@ -795,19 +932,19 @@ int launch(Layer& a, cudaStream_t stream) {
   if (int rc = check_launch()) return rc;
   int sms = 0;
   if (int rc = device_sm_count(&sms)) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms);
-  cfg.blockDim = dim3(kLayerThreads);
-  cfg.dynamicSmemBytes = kRingBytes;
-  cfg.stream = stream;
-  if (int rc = ensure_smem_limit((const void*)layer_experts<D>, kRingBytes)) return rc;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  (void)cudaLaunchKernelEx(&cfg, layer_experts<D>, a);
-  return check_launch();
+  WeightMaps maps = {};
+  if (a.hidden % 8 != 0 || a.ld_x % 8 != 0 || a.inter % 8 != 0 || !aligned16(a.x) ||
+      !aligned16(a.w1) || !aligned16(a.w2))
+    return launch_experts<D, kAny>(a, maps, sms, stream);
+  // tiles of 16 rows for a few tokens whose experts make few tiles of 64: with fewer than 8 of
+  // these a CTA, the last round would leave up to an eighth of the time of some CTAs idle
+  const int64_t experts = a.E < (int64_t)a.tokens * a.K ? a.E : a.tokens * a.K;
+  if ((a.tokens <= kNarrowTokens && experts * ((a.inter + 31) / 32) < 8 * (int64_t)sms) ||
+      a.inter == 0)
+    return launch_experts<D, kNarrow>(a, maps, sms, stream);
+  if (int rc = weight_map(&maps.w1, a.w1, a.hidden, a.inter, 2 * (int64_t)a.E, 32)) return rc;
+  if (int rc = weight_map(&maps.w2, a.w2, a.inter, a.hidden, a.E, 64)) return rc;
+  return launch_experts<D, kWide>(a, maps, sms, stream);
 }
 
 }  // namespace
@@ -839,7 +976,6 @@ int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream) {
   a.h = reinterpret_cast<uint16_t*>(ws + s.h);
   a.y = reinterpret_cast<float*>(ws + s.y);
   a.ld_h = (m.inter + 7) / 8 * 8;
-  a.aligned_x = aligned16(m.x); a.aligned_w1 = aligned16(m.w1); a.aligned_w2 = aligned16(m.w2);
   a.logits = m.router_w ? a.own_logits : m.logits;
   a.logits_dt = m.router_w ? MOE_FP32 : m.logits_dt;
   a.ld_logits = m.router_w ? m.E : m.ld_logits;
