@@ -125,6 +125,8 @@ int launch_residual_add(const void* e, const void* s, const void* r, void* out, 
                         moe_dtype dt, cudaStream_t stream);
 // fp32 bytes of the row groups' partial parameter gradients.
 int64_t layer_norm_bwd_workspace(int64_t rows, int64_t hidden);
+// Copies (and optionally clears) the layer norm's per-device timeout word.
+int layer_norm_device_errors(int32_t* bits, int clear);
 int launch_layer_norm_fwd(const void* x, const void* w, const void* b, void* y, float* mean,
                           float* rstd, int64_t rows, int64_t hidden, int64_t ld_x, int64_t ld_y,
                           float eps, moe_dtype dt, moe_dtype w_dt, cudaStream_t stream);

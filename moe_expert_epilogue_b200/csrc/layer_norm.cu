@@ -8,12 +8,22 @@
 //
 // All sums are fp32.  The variance is taken around the mean in a second pass
 // (E[x^2] - mean^2 loses every digit of rows whose mean is large).  The
-// parameter gradients are summed in two fixed steps: kNormGroups groups of
-// rows (group g holds rows g, g + kNormGroups, ...), each in row order, then
-// the groups' partial sums in group order.  The number of groups is a
-// constant, so the bits depend neither on the launch nor on the device.
+// parameter gradients are summed in two fixed steps: up to kNormGroups groups of
+// rows, each in row order, then the groups' partial sums in group order.  The
+// number of groups follows from the sizes alone, so the bits depend neither on
+// the launch nor on the device.
+//
+// HBM bandwidth bounds both passes: the rows are read once, held in registers,
+// and written once.  A warp holds a short row, a CTA a long one; a thread loads
+// 8 consecutive elements at a time, or single ones where the rows do not start
+// on 16-byte boundaries or the width is no multiple of 8.  Rows beyond 8192
+// (16384: forward, in eights) elements take the *_any kernels, which read them
+// again for each pass.
+#include <initializer_list>
+
 #include "common.cuh"
 #include "launch.cuh"
+#include "tma.cuh"
 
 namespace moe {
 
@@ -21,7 +31,14 @@ namespace {
 
 constexpr int kNormGroups = 148;   // row groups of the parameter gradients (one per SM)
 
-inline int norm_groups(int64_t rows) { return (int)(rows < kNormGroups ? rows : kNormGroups); }
+// Groups of `rows` rows that are taken `at_once` at a time.
+inline int norm_groups(int64_t rows, int at_once = 1) {
+  const int64_t n = (rows + at_once - 1) / at_once;
+  return (int)(n < kNormGroups ? n : kNormGroups);
+}
+
+// Error bits of waits that gave up (read by moe_device_errors).
+__device__ int32_t g_norm_errors;
 
 // Sum over the CTA's threads, the same on every thread; `red` is one slot of
 // a double buffer (a caller alternates two of them between barriers).
@@ -116,6 +133,297 @@ norm_bwd_cols_any(const typename D::T* __restrict__ gy, const typename D::T* __r
   pb[(int64_t)blockIdx.y * hidden + h] = db;
 }
 
+// ------------------------------------------------------------ rows in registers
+
+// VEC consecutive elements: raw bits as loaded, and widened.
+template <class D, int VEC> struct Unit;
+template <class D> struct Unit<D, 8> {
+  Raw8<D> raw;
+  __device__ __forceinline__ void load(const typename D::T* p) { raw = load8<D>(p); }
+  __device__ __forceinline__ void load_shared(const typename D::T* p) { raw = tma::lds8<D>(p); }
+  // a parameter: read by every row, so kept in L1
+  __device__ __forceinline__ void load_param(const typename D::T* p) {
+#pragma unroll
+    for (int i = 0; i < D::kBytes / 2; ++i) raw.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void widen(float (&v)[8]) const { widen8<D>(raw, v); }
+  static __device__ __forceinline__ void store(typename D::T* p, const float (&v)[8]) {
+    store8<D>(p, v);
+  }
+};
+template <class D> struct Unit<D, 1> {
+  float v0;
+  __device__ __forceinline__ void load(const typename D::T* p) { v0 = load1<D>(p); }
+  __device__ __forceinline__ void load_param(const typename D::T* p) { v0 = load1<D>(p); }
+  __device__ __forceinline__ void widen(float (&v)[1]) const { v[0] = v0; }
+  static __device__ __forceinline__ void store(typename D::T* p, const float (&v)[1]) {
+    store1<D>(p, v[0]);
+  }
+};
+
+// TPR threads (a warp or the CTA) per row, C units of VEC elements per thread;
+// the next row is loaded while this one is reduced.
+template <class D, class W, int VEC, int C, int TPR>
+__global__ void __launch_bounds__(kThreads)
+norm_fwd_rows(const typename D::T* __restrict__ x, const typename W::T* __restrict__ w,
+              const typename W::T* __restrict__ b, typename D::T* __restrict__ y,
+              float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t rows,
+              int hidden, int64_t ld_x, int64_t ld_y, float eps) {
+  pdl_prologue();
+  __shared__ float red[2][kThreads / 32];
+  const int t = threadIdx.x % TPR;
+  constexpr int kRows = kThreads / TPR;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  Unit<D, VEC> next[C];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) next[c].load(x + row * ld_x + h);
+    }
+  };
+  auto sum = [&](float v, float* slot) { return TPR == 32 ? warp_sum(v) : cta_sum(v, slot); };
+  if (r < rows) load(r);
+  for (; r < rows; r += step) {
+    float v[C][VEC];
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if ((c * TPR + t) * VEC < hidden) {
+        next[c].widen(v[c]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s += v[c][i];
+      }
+    }
+    if (r + step < rows) load(r + step);
+    const float mean = sum(s, red[0]) / (float)hidden;
+    s = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if ((c * TPR + t) * VEC < hidden) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          v[c][i] -= mean;
+          s = fmaf(v[c][i], v[c][i], s);
+        }
+      }
+    }
+    const float rstd = __frsqrt_rn(sum(s, red[1]) / (float)hidden + eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) {
+        Unit<W, VEC> u;
+        float p[VEC];
+        u.load_param(w + h);
+        u.widen(p);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[c][i] = v[c][i] * rstd * p[i];
+        if (b) {
+          u.load_param(b + h);
+          u.widen(p);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[c][i] += p[i];
+        }
+        Unit<D, VEC>::store(y + r * ld_y + h, v[c]);
+      }
+    }
+    if (t == 0) {
+      if (mean_out) mean_out[r] = mean;
+      if (rstd_out) rstd_out[r] = rstd;
+    }
+  }
+}
+
+// Backward.  One CTA of 16 warps per row group; WPR warps hold a row, so that
+// 16 / WPR rows are in work at a time, each thread with C units of VEC columns
+// and their shares of the parameter gradients in registers for all its rows.
+// With VEC = 8 the rows of x and grad_y come through a ring of `stages` stages
+// in shared memory (bulk copies, the refill issued as soon as the row's threads
+// have met at their reduction); single elements are loaded a row ahead.
+constexpr int kBwdThreads = 512;
+constexpr int kBwdRing = 200 * 1024;
+
+template <class D, class W, int VEC, int C, int WPR>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restrict__ x,
+              const typename W::T* __restrict__ w, const float* __restrict__ mean,
+              const float* __restrict__ rstd, typename D::T* __restrict__ gx,
+              float* __restrict__ pw, float* __restrict__ pb, int64_t rows, int hidden,
+              int64_t ld_gy, int64_t ld_x, int64_t ld_gx, int stages) {
+  using T = typename D::T;
+  constexpr int kTeams = kBwdThreads / 32 / WPR, TPR = WPR * 32;
+  constexpr bool kRing = VEC == 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[2][kBwdThreads / 32];
+  __shared__ uint64_t bars[kTeams * 8];
+  const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  if (kRing && threadIdx.x == 0) {
+    for (int i = 0; i < kTeams * 8; ++i) tma::mbar_init(&bars[i], 1);
+    tma::mbar_init_fence();
+  }
+  pdl_prologue();
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams;
+  const int64_t n = rows > first ? (rows - 1 - first) / step + 1 : 0;
+  const uint32_t row_bytes = (uint32_t)hidden * sizeof(T);
+  uint8_t* ring = smem + (size_t)team * stages * 2 * row_bytes;
+  uint64_t* full = bars + team * 8;
+  bool dead = false;
+  int64_t issued = 0;
+  auto issue = [&](int64_t k) {         // by the team's first thread
+    const int s = (int)(k % stages);
+    const int64_t r = first + k * step;
+    uint8_t* dst = ring + (size_t)s * 2 * row_bytes;
+    tma::mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
+    tma::bulk_load(dst, x + r * ld_x, row_bytes, &full[s]);
+    tma::bulk_load(dst + row_bytes, gy + r * ld_gy, row_bytes, &full[s]);
+    issued = k + 1;
+  };
+  Unit<D, VEC> nx[C], ng[C];
+  auto load = [&](int64_t k) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) {
+        nx[c].load(x + (first + k * step) * ld_x + h);
+        ng[c].load(gy + (first + k * step) * ld_gy + h);
+      }
+    }
+  };
+  if (kRing) {
+    if (t == 0)
+      for (int64_t k = 0; k < stages && k < n; ++k) issue(k);
+  } else if (n > 0) {
+    load(0);
+  }
+  float p[C][VEC], dw[C][VEC] = {}, db[C][VEC] = {};
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int h = (c * TPR + t) * VEC;
+    if (h < hidden) {
+      Unit<W, VEC> u;
+      u.load_param(w + h);
+      u.widen(p[c]);
+    }
+  }
+  float m = n > 0 ? __ldg(mean + first) : 0.f, rs = n > 0 ? __ldg(rstd + first) : 0.f;
+  const float inv = 1.0f / (float)hidden;
+  for (int64_t k = 0; k < n; ++k) {
+    const int64_t r = first + k * step;
+    const float row_m = m, row_rs = rs;
+    if (k + 1 < n) {
+      m = __ldg(mean + r + step);
+      rs = __ldg(rstd + r + step);
+    }
+    if constexpr (kRing) {
+      const int s = (int)(k % stages);
+      if (!dead && !tma::mbar_wait(&full[s], (uint32_t)(k / stages) & 1)) {
+        atomicOr(&g_norm_errors, MOE_DEVERR_TIMEOUT);
+        dead = true;
+      }
+      const T* row = reinterpret_cast<const T*>(ring + (size_t)s * 2 * row_bytes);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int h = (c * TPR + t) * VEC;
+        if (h < hidden) {
+          nx[c].load_shared(row + h);
+          ng[c].load_shared(row + hidden + h);
+        }
+      }
+    }
+    float a[C][VEC], xh[C][VEC];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if ((c * TPR + t) * VEC < hidden) {
+        nx[c].widen(xh[c]);
+        ng[c].widen(a[c]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float g = a[c][i];
+          xh[c][i] = (xh[c][i] - row_m) * row_rs;
+          a[c][i] = g * p[c][i];
+          s1 += a[c][i];
+          s2 = fmaf(a[c][i], xh[c][i], s2);
+          dw[c][i] = fmaf(g, xh[c][i], dw[c][i]);
+          db[c][i] += g;
+        }
+      }
+    }
+    if (!kRing && k + 1 < n) load(k + 1);
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (WPR == 1) {
+      __syncwarp();                       // the team has read its stage
+    } else {
+      float2* slot = red[k & 1] + team * WPR;
+      if ((t & 31) == 0) slot[t >> 5] = make_float2(s1, s2);
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TPR) : "memory");
+      s1 = s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) {
+        s1 += slot[i].x;
+        s2 += slot[i].y;
+      }
+    }
+    if (kRing && t == 0 && !dead && k + stages < n) issue(k + stages);
+    s1 *= inv;
+    s2 *= inv;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) a[c][i] = row_rs * (a[c][i] - s1 - xh[c][i] * s2);
+        Unit<D, VEC>::store(gx + r * ld_gx + h, a[c]);
+      }
+    }
+  }
+  if (kRing && dead && t == 0)            // before the CTA ends, its copies land
+    for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
+      tma::mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1);
+  pw += (int64_t)blockIdx.x * hidden;
+  pb += (int64_t)blockIdx.x * hidden;
+  if constexpr (kTeams == 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          pw[h + i] = dw[c][i];
+          pb[h + i] = db[c][i];
+        }
+      }
+    }
+  } else {                                // the teams' shares, in their order
+    __syncthreads();
+    float* all = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          all[team * hidden + h + i] = dw[c][i];
+          all[(kTeams + team) * hidden + h + i] = db[c][i];
+        }
+      }
+    }
+    __syncthreads();
+    for (int h = threadIdx.x; h < 2 * hidden; h += kBwdThreads) {
+      const bool bias = h >= hidden;
+      const float* v = all + (bias ? kTeams * hidden + h - hidden : h);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTeams; ++i) s += v[i * hidden];
+      (bias ? pb + h - hidden : pw + h)[0] = s;
+    }
+  }
+}
+
 // Sums the groups' partials of 32 columns per CTA: warp i takes the groups
 // i, i + 8, ..., in order, and the eight warps' sums are added in warp order.
 template <class W>
@@ -152,16 +460,46 @@ norm_bwd_groups(const float* __restrict__ pw, const float* __restrict__ pb,
 
 // ------------------------------------------------------------ launchers
 
+// In eights where every row and parameter starts on a 16-byte boundary.
+inline bool eights(int64_t hidden, std::initializer_list<const void*> ps,
+                   std::initializer_list<int64_t> lds) {
+  bool ok = hidden % kVec == 0;
+  for (const void* p : ps) ok = ok && aligned16(p);
+  for (int64_t ld : lds) ok = ok && ld % kVec == 0;
+  return ok;
+}
+
 template <class D, class W>
-int fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+int fwd(const void* x_, const void* w_, const void* b_, void* y_, float* mean, float* rstd,
         int64_t rows, int64_t hidden, int64_t ld_x, int64_t ld_y, float eps,
         cudaStream_t stream) {
-  auto k = norm_fwd_any<D, W>;
+  const auto* x = static_cast<const typename D::T*>(x_);
+  const auto *w = static_cast<const typename W::T*>(w_), *b = static_cast<const typename W::T*>(b_);
+  auto* y = static_cast<typename D::T*>(y_);
   int grid = 0;
+  auto rows_in_registers = [&](auto k, int per_cta) {
+    if (int rc = persistent_grid((const void*)k, 0, (rows + per_cta - 1) / per_cta, &grid))
+      return rc;
+    launch_kernel(k, grid, 0, stream, x, w, b, y, mean, rstd, rows, (int)hidden, ld_x, ld_y, eps);
+    return check_launch();
+  };
+  if (eights(hidden, {x, w, b, y}, {ld_x, ld_y}) && hidden <= 16384) {
+    const int64_t n = hidden / kVec;
+    if (n <= 32) return rows_in_registers(norm_fwd_rows<D, W, 8, 1, 32>, 8);
+    if (n <= 64) return rows_in_registers(norm_fwd_rows<D, W, 8, 2, 32>, 8);
+    if (n <= 128) return rows_in_registers(norm_fwd_rows<D, W, 8, 4, 32>, 8);
+    if (n <= 256) return rows_in_registers(norm_fwd_rows<D, W, 8, 1, 256>, 1);
+    if (n <= 512) return rows_in_registers(norm_fwd_rows<D, W, 8, 2, 256>, 1);
+    if (n <= 1024) return rows_in_registers(norm_fwd_rows<D, W, 8, 4, 256>, 1);
+    return rows_in_registers(norm_fwd_rows<D, W, 8, 8, 256>, 1);
+  }
+  if (hidden <= 256) return rows_in_registers(norm_fwd_rows<D, W, 1, 8, 32>, 8);
+  if (hidden <= 1024) return rows_in_registers(norm_fwd_rows<D, W, 1, 4, 256>, 1);
+  if (hidden <= 4096) return rows_in_registers(norm_fwd_rows<D, W, 1, 16, 256>, 1);
+  if (hidden <= 8192) return rows_in_registers(norm_fwd_rows<D, W, 1, 32, 256>, 1);
+  auto k = norm_fwd_any<D, W>;
   if (int rc = persistent_grid((const void*)k, 0, rows, &grid)) return rc;
-  launch_kernel(k, grid, 0, stream, static_cast<const typename D::T*>(x),
-                static_cast<const typename W::T*>(w), static_cast<const typename W::T*>(b),
-                static_cast<typename D::T*>(y), mean, rstd, rows, hidden, ld_x, ld_y, eps);
+  launch_kernel(k, grid, 0, stream, x, w, b, y, mean, rstd, rows, hidden, ld_x, ld_y, eps);
   return check_launch();
 }
 
@@ -173,17 +511,47 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
   const auto* x = static_cast<const typename D::T*>(x_);
   const auto* w = static_cast<const typename W::T*>(w_);
   auto* gx = static_cast<typename D::T*>(gx_);
-  const int groups = norm_groups(rows);
-  float *pw = ws, *pb = ws + groups * hidden;
-  int grid = 0;
-  auto kr = norm_bwd_rows_any<D, W>;
-  if (int rc = persistent_grid((const void*)kr, 0, rows, &grid)) return rc;
-  launch_kernel(kr, grid, 0, stream, gy, x, w, mean, rstd, gx, rows, hidden, ld_gy, ld_x, ld_gx);
-  if (int rc = check_launch()) return rc;
-  const dim3 cols((unsigned)((hidden + kThreads - 1) / kThreads), (unsigned)groups);
-  launch_kernel_grid(norm_bwd_cols_any<D>, cols, kThreads, 0, stream, gy, x, mean, rstd, pw, pb,
-                     rows, hidden, ld_gy, ld_x);
-  if (int rc = check_launch()) return rc;
+  int groups = 0;
+  float *pw = ws, *pb = nullptr;
+  auto rows_in_registers = [&](auto k, int vec, int teams) {
+    groups = norm_groups(rows, teams);
+    pb = ws + groups * hidden;
+    const int64_t stage = 2 * teams * hidden * (int64_t)sizeof(typename D::T);
+    const int stages = vec == 8 ? (int)(kBwdRing / stage < 8 ? kBwdRing / stage : 8) : 0;
+    // the ring, afterwards the teams' shares of the parameter gradients
+    int64_t smem = stages * stage;
+    if (teams > 1 && smem < 2 * teams * hidden * 4) smem = 2 * teams * hidden * 4;
+    if (int rc = ensure_smem_limit((const void*)k, kBwdRing)) return rc;
+    launch_kernel_block(k, groups, kBwdThreads, (size_t)smem, stream, gy, x, w, mean, rstd, gx, pw,
+                        pb, rows, (int)hidden, ld_gy, ld_x, ld_gx, stages);
+    return check_launch();
+  };
+  int rc = MOE_OK;
+  const bool vec = eights(hidden, {gy, x, w, gx}, {ld_gy, ld_x, ld_gx});
+  if (vec && hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 1>, 8, 16);
+  else if (vec && hidden <= 512) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 1>, 8, 16);
+  else if (vec && hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 4>, 8, 4);
+  else if (vec && hidden <= 2048) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 4>, 8, 4);
+  else if (vec && hidden <= 4096) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 16>, 8, 1);
+  else if (vec && hidden <= 8192) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 16>, 8, 1);
+  else if (hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 1>, 1, 16);
+  else if (hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 4>, 1, 4);
+  else if (hidden <= 4096) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 16>, 1, 1);
+  else if (hidden <= 8192) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 16, 16>, 1, 1);
+  else {
+    groups = norm_groups(rows);
+    pb = ws + groups * hidden;
+    int grid = 0;
+    auto kr = norm_bwd_rows_any<D, W>;
+    if (int e = persistent_grid((const void*)kr, 0, rows, &grid)) return e;
+    launch_kernel(kr, grid, 0, stream, gy, x, w, mean, rstd, gx, rows, hidden, ld_gy, ld_x, ld_gx);
+    if (int e = check_launch()) return e;
+    const dim3 cols((unsigned)((hidden + kThreads - 1) / kThreads), (unsigned)groups);
+    launch_kernel_grid(norm_bwd_cols_any<D>, cols, kThreads, 0, stream, gy, x, mean, rstd, pw, pb,
+                       rows, hidden, ld_gy, ld_x);
+    rc = check_launch();
+  }
+  if (rc) return rc;
   launch_kernel(norm_bwd_groups<W>, (int)((hidden + 31) / 32), 0, stream, (const float*)pw,
                 (const float*)pb, static_cast<typename W::T*>(gw_),
                 static_cast<typename W::T*>(gb_), groups, hidden);
@@ -194,6 +562,17 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
 
 int64_t layer_norm_bwd_workspace(int64_t rows, int64_t hidden) {
   return 2 * (int64_t)norm_groups(rows) * hidden * (int64_t)sizeof(float);
+}
+
+int layer_norm_device_errors(int32_t* bits, int clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_norm_errors, sizeof(int32_t));
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (clear) {
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_norm_errors, &zero, sizeof(int32_t));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return MOE_OK;
 }
 
 #define MOE_NORM_DISPATCH(F, ...)                                                    \

@@ -660,5 +660,8 @@ extern "C" int moe_device_errors(int32_t* bits, int clear) {
   int32_t epc = 0;
   if (int rc = moe::ep_combine_device_errors(&epc, clear)) return rc;
   *bits |= epc;
+  int32_t norm = 0;
+  if (int rc = moe::layer_norm_device_errors(&norm, clear)) return rc;
+  *bits |= norm;
   return MOE_OK;
 }
