@@ -236,12 +236,71 @@ norm_fwd_rows(const typename D::T* __restrict__ x, const typename W::T* __restri
   }
 }
 
-// Backward.  One CTA of 16 warps per row group; WPR warps hold a row, so that
-// 16 / WPR rows are in work at a time, each thread with C units of VEC columns
-// and their shares of the parameter gradients in registers for all its rows.
-// With VEC = 8 the rows of x and grad_y come through a ring of `stages` stages
-// in shared memory (bulk copies, the refill issued as soon as the row's threads
-// have met at their reduction); single elements are loaded a row ahead.
+// Packed pairs of fp32 (one instruction for both on sm_100), or single values.
+struct Two { unsigned long long v; };
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split2(const Two& a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return c;
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+
+// The VEC elements of a unit as pairs (VEC 8) or as they are (VEC 1).
+template <int VEC> struct Lanes;
+template <> struct Lanes<8> {
+  using T = Two;
+  static constexpr int N = 4;
+  static __device__ __forceinline__ Two all(float v) { return two(v, v); }
+  static __device__ __forceinline__ void pack(const float (&v)[8], Two (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = two(v[2 * i], v[2 * i + 1]);
+  }
+  static __device__ __forceinline__ void unpack(const Two (&v)[4], float (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2(v[i], o[2 * i], o[2 * i + 1]);
+  }
+  static __device__ __forceinline__ float total(const Two& a) {
+    float lo, hi;
+    split2(a, lo, hi);
+    return lo + hi;
+  }
+};
+template <> struct Lanes<1> {
+  using T = float;
+  static constexpr int N = 1;
+  static __device__ __forceinline__ float all(float v) { return v; }
+  static __device__ __forceinline__ void pack(const float (&v)[1], float (&o)[1]) { o[0] = v[0]; }
+  static __device__ __forceinline__ void unpack(const float (&v)[1], float (&o)[1]) { o[0] = v[0]; }
+  static __device__ __forceinline__ float total(float a) { return a; }
+};
+
+// Backward.  One CTA of 16 warps per row group; a team of WPR warps takes R rows
+// at a time, so that R * 16 / WPR rows are in work at once, each thread with C
+// units of VEC columns and their shares of the parameter gradients in registers
+// for all its rows.  With VEC = 8 the rows of x and grad_y come through a ring
+// of `stages` stages in shared memory (bulk copies, the refill issued as soon as
+// the team has met at its reduction); single elements are loaded a row ahead.
+// A row's chain (load, two sums over the team, finish) takes about 1 us in which
+// the team can do nothing else: with one row at a time, 16384 x 7168 bf16 took
+// 229 us; two rows of 16-bit elements share the chain.  The arithmetic is packed
+// in pairs, since its instructions alone would otherwise take half of the time.
 constexpr int kBwdThreads = 512;
 constexpr int kBwdRing = 200 * 1024;
 
@@ -253,10 +312,13 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
               float* __restrict__ pw, float* __restrict__ pb, int64_t rows, int hidden,
               int64_t ld_gy, int64_t ld_x, int64_t ld_gx, int stages) {
   using T = typename D::T;
-  constexpr int kTeams = kBwdThreads / 32 / WPR, TPR = WPR * 32;
+  using L = Lanes<VEC>;
+  using P = typename L::T;
+  constexpr int kTeams = kBwdThreads / 32 / WPR, TPR = WPR * 32, N = L::N;
   constexpr bool kRing = VEC == 8;
+  constexpr int R = kRing && D::kBytes == 2 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[2][kBwdThreads / 32];
+  __shared__ float2 red[2][R][kBwdThreads / 32];
   __shared__ uint64_t bars[kTeams * 8];
   const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
   if (kRing && threadIdx.x == 0) {
@@ -266,152 +328,199 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   pdl_prologue();
   __syncthreads();
   const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams;
-  const int64_t n = rows > first ? (rows - 1 - first) / step + 1 : 0;
+  const int n = rows > first ? (int)((rows - 1 - first) / step + 1) : 0;
   const uint32_t row_bytes = (uint32_t)hidden * sizeof(T);
   uint8_t* ring = smem + (size_t)team * stages * 2 * row_bytes;
   uint64_t* full = bars + team * 8;
   bool dead = false;
-  int64_t issued = 0;
-  auto issue = [&](int64_t k) {         // by the team's first thread
-    const int s = (int)(k % stages);
-    const int64_t r = first + k * step;
-    uint8_t* dst = ring + (size_t)s * 2 * row_bytes;
-    tma::mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
-    tma::bulk_load(dst, x + r * ld_x, row_bytes, &full[s]);
-    tma::bulk_load(dst + row_bytes, gy + r * ld_gy, row_bytes, &full[s]);
-    issued = k + 1;
+  // The stages are used in turn: `put` and `get` walk through them.
+  int put = 0, get = 0, issued = 0;
+  uint32_t parity = 0;
+  auto issue = [&] {                      // the next row's copies; by the team's first thread
+    const int64_t r = first + issued * step;
+    uint8_t* dst = ring + (size_t)put * 2 * row_bytes;
+    tma::mbar_arrive_expect_tx(&full[put], 2 * row_bytes);
+    tma::bulk_load(dst, x + r * ld_x, row_bytes, &full[put]);
+    tma::bulk_load(dst + row_bytes, gy + r * ld_gy, row_bytes, &full[put]);
+    ++issued;
+    if (++put == stages) put = 0;
   };
-  Unit<D, VEC> nx[C], ng[C];
-  auto load = [&](int64_t k) {
+  Unit<D, VEC> nx[R][C], ng[R][C];
+  auto load = [&](int k) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int h = (c * TPR + t) * VEC;
       if (h < hidden) {
-        nx[c].load(x + (first + k * step) * ld_x + h);
-        ng[c].load(gy + (first + k * step) * ld_gy + h);
+        nx[0][c].load(x + (first + k * step) * ld_x + h);
+        ng[0][c].load(gy + (first + k * step) * ld_gy + h);
       }
     }
   };
   if (kRing) {
     if (t == 0)
-      for (int64_t k = 0; k < stages && k < n; ++k) issue(k);
+      while (issued < stages && issued < n) issue();
   } else if (n > 0) {
     load(0);
   }
-  float p[C][VEC], dw[C][VEC] = {}, db[C][VEC] = {};
+  P p[C][N], dw[C][N], db[C][N];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int h = (c * TPR + t) * VEC;
     if (h < hidden) {
       Unit<W, VEC> u;
+      float v[VEC];
       u.load_param(w + h);
-      u.widen(p[c]);
+      u.widen(v);
+      L::pack(v, p[c]);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[c][i] = db[c][i] = L::all(0.f);
   }
-  float m = n > 0 ? __ldg(mean + first) : 0.f, rs = n > 0 ? __ldg(rstd + first) : 0.f;
-  const float inv = 1.0f / (float)hidden;
-  for (int64_t k = 0; k < n; ++k) {
-    const int64_t r = first + k * step;
-    const float row_m = m, row_rs = rs;
-    if (k + 1 < n) {
-      m = __ldg(mean + r + step);
-      rs = __ldg(rstd + r + step);
+  float m[R], rs[R];
+  auto stats = [&](int k) {               // (a row past the last has zeros)
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      m[q] = k + q < n ? __ldg(mean + first + (k + q) * step) : 0.f;
+      rs[q] = k + q < n ? __ldg(rstd + first + (k + q) * step) : 0.f;
     }
+  };
+  stats(0);
+  const float inv = 1.0f / (float)hidden;
+  for (int k = 0; k < n; k += R) {
+    float row_m[R], row_rs[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      row_m[q] = m[q];
+      row_rs[q] = rs[q];
+    }
+    if (k + R < n) stats(k + R);
     if constexpr (kRing) {
-      const int s = (int)(k % stages);
-      if (!dead && !tma::mbar_wait(&full[s], (uint32_t)(k / stages) & 1)) {
-        atomicOr(&g_norm_errors, MOE_DEVERR_TIMEOUT);
-        dead = true;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (k + q >= n) break;
+        if (!dead && !tma::mbar_wait(&full[get], parity)) {
+          atomicOr(&g_norm_errors, MOE_DEVERR_TIMEOUT);
+          dead = true;
+        }
+        const T* row = reinterpret_cast<const T*>(ring + (size_t)get * 2 * row_bytes);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int h = (c * TPR + t) * VEC;
+          if (h < hidden) {
+            nx[q][c].load_shared(row + h);
+            ng[q][c].load_shared(row + hidden + h);
+          }
+        }
+        if (++get == stages) { get = 0; parity ^= 1u; }
       }
-      const T* row = reinterpret_cast<const T*>(ring + (size_t)s * 2 * row_bytes);
+    }
+    Unit<D, VEC> keep_x[R][C], keep_g[R][C];
+    float s1[R], s2[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      P t1 = L::all(0.f), t2 = L::all(0.f);
+      const P sub = L::all(-row_m[q]), scale = L::all(row_rs[q]);
+      if (k + q < n) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if ((c * TPR + t) * VEC < hidden) {
+            float v[VEC];
+            P xv[N], gv[N];
+            nx[q][c].widen(v);
+            L::pack(v, xv);
+            ng[q][c].widen(v);
+            L::pack(v, gv);
+            keep_x[q][c] = nx[q][c];
+            keep_g[q][c] = ng[q][c];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const P g_xh = mul(gv[i], mul(add(xv[i], sub), scale));
+              dw[c][i] = add(dw[c][i], g_xh);
+              db[c][i] = add(db[c][i], gv[i]);
+              t1 = fma(gv[i], p[c][i], t1);
+              t2 = fma(g_xh, p[c][i], t2);
+            }
+          }
+        }
+      }
+      s1[q] = L::total(t1);
+      s2[q] = L::total(t2);
+    }
+    if (!kRing && k + 1 < n) load(k + 1);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      s1[q] = warp_sum(s1[q]);
+      s2[q] = warp_sum(s2[q]);
+    }
+    if constexpr (WPR == 1) {
+      __syncwarp();                       // the team has read its stages
+    } else {
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        if ((t & 31) == 0) red[k / R & 1][q][threadIdx.x >> 5] = make_float2(s1[q], s2[q]);
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TPR) : "memory");
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        s1[q] = s2[q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+          const float2 v = red[k / R & 1][q][team * WPR + i];
+          s1[q] += v.x;
+          s2[q] += v.y;
+        }
+      }
+    }
+    if (kRing && t == 0 && !dead)
+      for (int q = 0; q < R && issued < n; ++q) issue();
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (k + q >= n) break;
+      const P sub = L::all(-row_m[q]), scale = L::all(row_rs[q]);
+      const P a1 = L::all(-s1[q] * inv), a2 = L::all(-s2[q] * inv);
+      T* out = gx + (first + (k + q) * step) * ld_gx;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int h = (c * TPR + t) * VEC;
         if (h < hidden) {
-          nx[c].load_shared(row + h);
-          ng[c].load_shared(row + hidden + h);
+          float v[VEC];
+          P xv[N], gv[N];
+          keep_x[q][c].widen(v);
+          L::pack(v, xv);
+          keep_g[q][c].widen(v);
+          L::pack(v, gv);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const P xh = mul(add(xv[i], sub), scale);
+            xv[i] = mul(scale, add(fma(gv[i], p[c][i], a1), mul(xh, a2)));
+          }
+          L::unpack(xv, v);
+          Unit<D, VEC>::store(out + h, v);
         }
-      }
-    }
-    float a[C][VEC], xh[C][VEC];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if ((c * TPR + t) * VEC < hidden) {
-        nx[c].widen(xh[c]);
-        ng[c].widen(a[c]);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float g = a[c][i];
-          xh[c][i] = (xh[c][i] - row_m) * row_rs;
-          a[c][i] = g * p[c][i];
-          s1 += a[c][i];
-          s2 = fmaf(a[c][i], xh[c][i], s2);
-          dw[c][i] = fmaf(g, xh[c][i], dw[c][i]);
-          db[c][i] += g;
-        }
-      }
-    }
-    if (!kRing && k + 1 < n) load(k + 1);
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (WPR == 1) {
-      __syncwarp();                       // the team has read its stage
-    } else {
-      float2* slot = red[k & 1] + team * WPR;
-      if ((t & 31) == 0) slot[t >> 5] = make_float2(s1, s2);
-      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TPR) : "memory");
-      s1 = s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < WPR; ++i) {
-        s1 += slot[i].x;
-        s2 += slot[i].y;
-      }
-    }
-    if (kRing && t == 0 && !dead && k + stages < n) issue(k + stages);
-    s1 *= inv;
-    s2 *= inv;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + t) * VEC;
-      if (h < hidden) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) a[c][i] = row_rs * (a[c][i] - s1 - xh[c][i] * s2);
-        Unit<D, VEC>::store(gx + r * ld_gx + h, a[c]);
       }
     }
   }
   if (kRing && dead && t == 0)            // before the CTA ends, its copies land
-    for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
+    for (int k = issued > stages ? issued - stages : 0; k < issued; ++k)
       tma::mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1);
   pw += (int64_t)blockIdx.x * hidden;
   pb += (int64_t)blockIdx.x * hidden;
-  if constexpr (kTeams == 1) {
+  if constexpr (kTeams > 1) __syncthreads();   // every team is done with its ring
+  float* all = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + t) * VEC;
-      if (h < hidden) {
+  for (int c = 0; c < C; ++c) {
+    const int h = (c * TPR + t) * VEC;
+    if (h < hidden) {
+      float vw[VEC], vb[VEC];
+      L::unpack(dw[c], vw);
+      L::unpack(db[c], vb);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          pw[h + i] = dw[c][i];
-          pb[h + i] = db[c][i];
-        }
+      for (int i = 0; i < VEC; ++i) {
+        (kTeams == 1 ? pw : all + team * hidden)[h + i] = vw[i];
+        (kTeams == 1 ? pb : all + (kTeams + team) * hidden)[h + i] = vb[i];
       }
     }
-  } else {                                // the teams' shares, in their order
-    __syncthreads();
-    float* all = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + t) * VEC;
-      if (h < hidden) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          all[team * hidden + h + i] = dw[c][i];
-          all[(kTeams + team) * hidden + h + i] = db[c][i];
-        }
-      }
-    }
+  }
+  if constexpr (kTeams > 1) {             // the teams' shares, in their order
     __syncthreads();
     for (int h = threadIdx.x; h < 2 * hidden; h += kBwdThreads) {
       const bool bias = h >= hidden;
