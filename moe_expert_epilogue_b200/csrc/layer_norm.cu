@@ -302,7 +302,57 @@ template <> struct Lanes<1> {
 // 229 us; two rows of 16-bit elements share the chain.  The arithmetic is packed
 // in pairs, since its instructions alone would otherwise take half of the time.
 constexpr int kBwdThreads = 512;
-constexpr int kBwdRing = 200 * 1024;
+constexpr int kBwdSmem = 224 * 1024;      // the ring, then the weights in fp32
+
+// Sums s1[q], s2[q] of R rows over a team of WPR warps, on every thread.  The 2 R
+// values share the butterflies: its first steps halve the values a lane goes on
+// with, so that a warp's part takes 3 + 3 R shuffles instead of 10 R.  A value's
+// tree is the same whichever of the rows it belongs to.  `slots`: this turn's
+// half of a double buffer, [warp][2 R].
+template <int R, int WPR>
+__device__ __forceinline__ void team_sums(float (&s1)[R], float (&s2)[R], float* slots, int team) {
+  constexpr int V = 2 * R;
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float v;
+  int mine;
+  if constexpr (R == 2) {
+    const bool up = lane & 16;
+    const float a = (up ? s1[1] : s1[0]) + __shfl_xor_sync(kAll, up ? s1[0] : s1[1], 16);
+    const float b = (up ? s2[1] : s2[0]) + __shfl_xor_sync(kAll, up ? s2[0] : s2[1], 16);
+    v = (lane & 8 ? b : a) + __shfl_xor_sync(kAll, lane & 8 ? a : b, 8);
+    mine = lane >> 3;                     // s1[0], s2[0], s1[1], s2[1]
+  } else {
+    v = (lane & 16 ? s2[0] : s1[0]) + __shfl_xor_sync(kAll, lane & 16 ? s1[0] : s2[0], 16);
+    v += __shfl_xor_sync(kAll, v, 8);
+    mine = lane >> 4;
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  constexpr int kSpread = 32 / V;         // lanes that hold one value
+  if constexpr (WPR == 1) {
+    __syncwarp();                         // the team has read its stages
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      s1[q] = __shfl_sync(kAll, v, 2 * q * kSpread);
+      s2[q] = __shfl_sync(kAll, v, (2 * q + 1) * kSpread);
+    }
+  } else {
+    if (lane % kSpread == 0) slots[warp * V + mine] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(WPR * 32) : "memory");
+    constexpr int kAtOnce = kSpread < WPR ? kSpread : WPR;    // warps' values that lanes load
+    const float* first = slots + (team * WPR + lane / V % kAtOnce) * V + lane % V;
+    v = first[0];
+    if constexpr (WPR > kAtOnce) v += first[kAtOnce * V];
+#pragma unroll
+    for (int o = V; o < V * kAtOnce; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      s1[q] = __shfl_sync(kAll, v, 2 * q);
+      s2[q] = __shfl_sync(kAll, v, 2 * q + 1);
+    }
+  }
+}
 
 template <class D, class W, int VEC, int C, int WPR>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -318,7 +368,7 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   constexpr bool kRing = VEC == 8;
   constexpr int R = kRing && D::kBytes == 2 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[2][R][kBwdThreads / 32];
+  __shared__ float red[2][kBwdThreads / 32 * 2 * R];
   __shared__ uint64_t bars[kTeams * 8];
   const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
   if (kRing && threadIdx.x == 0) {
@@ -362,20 +412,47 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   } else if (n > 0) {
     load(0);
   }
-  P p[C][N], dw[C][N], db[C][N];
+  // With VEC = 8 the weights lie in shared memory (a unit's halves in two planes,
+  // free of bank conflicts), else in registers.
+  float4* const weights = reinterpret_cast<float4*>(smem + (size_t)kTeams * stages * 2 * row_bytes);
+  const int units = hidden / 8;
+  P kept[kRing ? 1 : C][N];
+  if constexpr (kRing) {
+    for (int c = threadIdx.x; c < units; c += kBwdThreads) {
+      Unit<W, VEC> u;
+      float v[8];
+      u.load_param(w + c * 8);
+      u.widen(reinterpret_cast<float (&)[VEC]>(v));
+      weights[c] = make_float4(v[0], v[1], v[2], v[3]);
+      weights[units + c] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __syncthreads();
+  }
+  P dw[C][N], db[C][N];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int h = (c * TPR + t) * VEC;
-    if (h < hidden) {
-      Unit<W, VEC> u;
-      float v[VEC];
-      u.load_param(w + h);
-      u.widen(v);
-      L::pack(v, p[c]);
+    if constexpr (!kRing) {
+      if (h < hidden) {
+        Unit<W, VEC> u;
+        float v[VEC];
+        u.load_param(w + h);
+        u.widen(v);
+        L::pack(v, kept[c]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[c][i] = db[c][i] = L::all(0.f);
   }
+  auto param = [&](int c, P (&p)[N]) {
+    if constexpr (kRing) {
+      const float4 lo = weights[c * TPR + t], hi = weights[units + c * TPR + t];
+      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      L::pack(reinterpret_cast<const float (&)[VEC]>(v), p);
+    } else {
+      p[0] = kept[c][0];
+    }
+  };
   float m[R], rs[R];
   auto stats = [&](int k) {               // (a row past the last has zeros)
 #pragma unroll
@@ -414,87 +491,70 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
         if (++get == stages) { get = 0; parity ^= 1u; }
       }
     }
-    Unit<D, VEC> keep_x[R][C], keep_g[R][C];
+    P xh[R][C][N];
+    Unit<D, VEC> g_raw[R][C];
     float s1[R], s2[R];
+    P t1[R], t2[R];
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      P t1 = L::all(0.f), t2 = L::all(0.f);
-      const P sub = L::all(-row_m[q]), scale = L::all(row_rs[q]);
-      if (k + q < n) {
+    for (int q = 0; q < R; ++q) t1[q] = t2[q] = L::all(0.f);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if ((c * TPR + t) * VEC < hidden) {
-            float v[VEC];
-            P xv[N], gv[N];
-            nx[q][c].widen(v);
-            L::pack(v, xv);
-            ng[q][c].widen(v);
-            L::pack(v, gv);
-            keep_x[q][c] = nx[q][c];
-            keep_g[q][c] = ng[q][c];
+    for (int c = 0; c < C; ++c) {
+      if ((c * TPR + t) * VEC < hidden) {
+        P p[N];
+        param(c, p);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const P g_xh = mul(gv[i], mul(add(xv[i], sub), scale));
-              dw[c][i] = add(dw[c][i], g_xh);
-              db[c][i] = add(db[c][i], gv[i]);
-              t1 = fma(gv[i], p[c][i], t1);
-              t2 = fma(g_xh, p[c][i], t2);
-            }
+        for (int q = 0; q < R; ++q) {
+          if (k + q >= n) break;
+          const P sub = L::all(-row_m[q]), scale = L::all(row_rs[q]);
+          float v[VEC];
+          P gv[N];
+          nx[q][c].widen(v);
+          L::pack(v, xh[q][c]);
+          g_raw[q][c] = ng[q][c];
+          ng[q][c].widen(v);
+          L::pack(v, gv);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            xh[q][c][i] = mul(add(xh[q][c][i], sub), scale);
+            const P g_xh = mul(gv[i], xh[q][c][i]);
+            dw[c][i] = add(dw[c][i], g_xh);
+            db[c][i] = add(db[c][i], gv[i]);
+            t1[q] = fma(gv[i], p[i], t1[q]);
+            t2[q] = fma(g_xh, p[i], t2[q]);
           }
         }
       }
-      s1[q] = L::total(t1);
-      s2[q] = L::total(t2);
     }
     if (!kRing && k + 1 < n) load(k + 1);
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      s1[q] = warp_sum(s1[q]);
-      s2[q] = warp_sum(s2[q]);
+      s1[q] = L::total(t1[q]);
+      s2[q] = L::total(t2[q]);
     }
-    if constexpr (WPR == 1) {
-      __syncwarp();                       // the team has read its stages
-    } else {
-#pragma unroll
-      for (int q = 0; q < R; ++q)
-        if ((t & 31) == 0) red[k / R & 1][q][threadIdx.x >> 5] = make_float2(s1[q], s2[q]);
-      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TPR) : "memory");
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        s1[q] = s2[q] = 0.f;
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) {
-          const float2 v = red[k / R & 1][q][team * WPR + i];
-          s1[q] += v.x;
-          s2[q] += v.y;
-        }
-      }
-    }
+    team_sums<R, WPR>(s1, s2, red[k / R & 1], team);
     if (kRing && t == 0 && !dead)
       for (int q = 0; q < R && issued < n; ++q) issue();
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      if (k + q >= n) break;
-      const P sub = L::all(-row_m[q]), scale = L::all(row_rs[q]);
-      const P a1 = L::all(-s1[q] * inv), a2 = L::all(-s2[q] * inv);
-      T* out = gx + (first + (k + q) * step) * ld_gx;
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + t) * VEC;
+      if (h < hidden) {
+        P p[N];
+        param(c, p);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int h = (c * TPR + t) * VEC;
-        if (h < hidden) {
+        for (int q = 0; q < R; ++q) {
+          if (k + q >= n) break;
+          // rstd (g p - mean(a) - xhat mean(a xhat))
+          const P scale = L::all(row_rs[q]);
+          const P a1 = L::all(-row_rs[q] * (s1[q] * inv)), a2 = L::all(-row_rs[q] * (s2[q] * inv));
           float v[VEC];
-          P xv[N], gv[N];
-          keep_x[q][c].widen(v);
-          L::pack(v, xv);
-          keep_g[q][c].widen(v);
+          P gv[N];
+          g_raw[q][c].widen(v);
           L::pack(v, gv);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const P xh = mul(add(xv[i], sub), scale);
-            xv[i] = mul(scale, add(fma(gv[i], p[c][i], a1), mul(xh, a2)));
-          }
-          L::unpack(xv, v);
-          Unit<D, VEC>::store(out + h, v);
+          for (int i = 0; i < N; ++i)
+            gv[i] = fma(xh[q][c][i], a2, fma(mul(gv[i], p[i]), scale, a1));
+          L::unpack(gv, v);
+          Unit<D, VEC>::store(gx + (first + (k + q) * step) * ld_gx + h, v);
         }
       }
     }
@@ -533,37 +593,38 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   }
 }
 
-// Sums the groups' partials of 32 columns per CTA: warp i takes the groups
-// i, i + 8, ..., in order, and the eight warps' sums are added in warp order.
+// Sums the groups' partials of 32 columns per CTA: warps 0 .. 15 the weight's,
+// the others the bias's; warp i takes the groups i, i + 16, ..., in order, and
+// the sixteen sums are added in warp order.
+constexpr int kSumThreads = 1024, kSumWarps = kSumThreads / 64;
+
 template <class W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSumThreads)
 norm_bwd_groups(const float* __restrict__ pw, const float* __restrict__ pb,
                 typename W::T* __restrict__ gw, typename W::T* __restrict__ gb, int groups,
                 int64_t hidden) {
   pdl_prologue();
-  __shared__ float sw[kThreads / 32][32], sb[kThreads / 32][32];
+  __shared__ float sums[2][kSumWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool bias = warp >= kSumWarps;
   const int64_t h = (int64_t)blockIdx.x * 32 + lane;
-  float dw = 0.f, db = 0.f;
-  if (h < hidden) {
-#pragma unroll 4
-    for (int g = warp; g < groups; g += kThreads / 32) {
-      dw += __ldg(pw + g * hidden + h);
-      db += __ldg(pb + g * hidden + h);
+  const float* src = bias ? pb : pw;
+  typename W::T* dst = bias ? gb : gw;
+  float s = 0.f;
+  if (h < hidden && dst) {
+#pragma unroll
+    for (int i = 0; i < (kNormGroups + kSumWarps - 1) / kSumWarps; ++i) {
+      const int g = i * kSumWarps + (warp & (kSumWarps - 1));
+      if (g < groups) s += __ldg(src + g * hidden + h);
     }
   }
-  sw[warp][lane] = dw;
-  sb[warp][lane] = db;
+  sums[bias][warp & (kSumWarps - 1)][lane] = s;
   __syncthreads();
-  if (warp == 0 && h < hidden) {
-    dw = db = 0.f;
+  if ((warp & (kSumWarps - 1)) == 0 && h < hidden && dst) {
+    s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      dw += sw[i][lane];
-      db += sb[i][lane];
-    }
-    store1<W>(gw + h, dw);
-    if (gb) store1<W>(gb + h, db);
+    for (int i = 0; i < kSumWarps; ++i) s += sums[bias][i][lane];
+    store1<W>(dst + h, s);
   }
 }
 
@@ -626,11 +687,12 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
     groups = norm_groups(rows, teams);
     pb = ws + groups * hidden;
     const int64_t stage = 2 * teams * hidden * (int64_t)sizeof(typename D::T);
-    const int stages = vec == 8 ? (int)(kBwdRing / stage < 8 ? kBwdRing / stage : 8) : 0;
-    // the ring, afterwards the teams' shares of the parameter gradients
-    int64_t smem = stages * stage;
+    const int64_t fit = (kBwdSmem - hidden * 4) / stage;
+    const int stages = vec == 8 ? (int)(fit < 8 ? fit : 8) : 0;
+    // the ring and the weights; afterwards the teams' shares of the parameter gradients
+    int64_t smem = vec == 8 ? stages * stage + hidden * 4 : 0;
     if (teams > 1 && smem < 2 * teams * hidden * 4) smem = 2 * teams * hidden * 4;
-    if (int rc = ensure_smem_limit((const void*)k, kBwdRing)) return rc;
+    if (int rc = ensure_smem_limit((const void*)k, kBwdSmem)) return rc;
     launch_kernel_block(k, groups, kBwdThreads, (size_t)smem, stream, gy, x, w, mean, rstd, gx, pw,
                         pb, rows, (int)hidden, ld_gy, ld_x, ld_gx, stages);
     return check_launch();
@@ -638,9 +700,9 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
   int rc = MOE_OK;
   const bool vec = eights(hidden, {gy, x, w, gx}, {ld_gy, ld_x, ld_gx});
   if (vec && hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 1>, 8, 16);
-  else if (vec && hidden <= 512) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 1>, 8, 16);
+  else if (vec && hidden <= 512) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 2>, 8, 8);
   else if (vec && hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 4>, 8, 4);
-  else if (vec && hidden <= 2048) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 4>, 8, 4);
+  else if (vec && hidden <= 2048) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 8>, 8, 2);
   else if (vec && hidden <= 4096) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 16>, 8, 1);
   else if (vec && hidden <= 8192) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 16>, 8, 1);
   else if (hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 1>, 1, 16);
@@ -661,9 +723,9 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
     rc = check_launch();
   }
   if (rc) return rc;
-  launch_kernel(norm_bwd_groups<W>, (int)((hidden + 31) / 32), 0, stream, (const float*)pw,
-                (const float*)pb, static_cast<typename W::T*>(gw_),
-                static_cast<typename W::T*>(gb_), groups, hidden);
+  launch_kernel_block(norm_bwd_groups<W>, (int)((hidden + 31) / 32), kSumThreads, 0, stream,
+                      (const float*)pw, (const float*)pb, static_cast<typename W::T*>(gw_),
+                      static_cast<typename W::T*>(gb_), groups, hidden);
   return check_launch();
 }
 
