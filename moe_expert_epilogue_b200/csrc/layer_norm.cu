@@ -291,68 +291,34 @@ template <> struct Lanes<1> {
   static __device__ __forceinline__ float total(float a) { return a; }
 };
 
-// Backward.  One CTA of 16 warps per row group; a team of WPR warps takes R rows
-// at a time, so that R * 16 / WPR rows are in work at once, each thread with C
-// units of VEC columns and their shares of the parameter gradients in registers
-// for all its rows.  With VEC = 8 the rows of x and grad_y come through a ring
-// of `stages` stages in shared memory (bulk copies, the refill issued as soon as
-// the team has met at its reduction); single elements are loaded a row ahead.
-// A row's chain (load, two sums over the team, finish) takes about 1 us in which
-// the team can do nothing else: with one row at a time, 16384 x 7168 bf16 took
-// 229 us; two rows of 16-bit elements share the chain.  The arithmetic is packed
-// in pairs, since its instructions alone would otherwise take half of the time.
-constexpr int kBwdThreads = 512;
-constexpr int kBwdSmem = 224 * 1024;      // the ring, then the weights in fp32
+// Backward.  One CTA of 16 warps per row group; a team of WPR warps takes a row,
+// so that 16 / WPR rows are in work at once, each thread with C units of VEC
+// columns and their shares of the parameter gradients in registers for all its
+// rows.
+//   gather(k)  row k's terms of the parameter gradients, and the two sums over
+//              this warp's columns
+//   finish(k)  the sums over the team, grad_x
+// With VEC = 8 the rows of x and grad_y come through a ring of `stages` stages in
+// shared memory (bulk copies) and finish reads them there again: registers go to
+// the gradients' shares, so that few warps hold a row and several rows' chains of
+// dependent steps (about 1 us each) overlap.  Single elements are loaded a row
+// ahead and kept in registers.  The arithmetic is packed in pairs (one
+// instruction for two elements).  At 16384 x 7168 bf16: one row at a time over 16
+// warps 229 us, over 32 warps 167, with the next row gathered first 169.
+constexpr int kBwdSmem = 222 * 1024;      // the ring, then the weights in fp32
 
-// Sums s1[q], s2[q] of R rows over a team of WPR warps, on every thread.  The 2 R
-// values share the butterflies: its first steps halve the values a lane goes on
-// with, so that a warp's part takes 3 + 3 R shuffles instead of 10 R.  A value's
-// tree is the same whichever of the rows it belongs to.  `slots`: this turn's
-// half of a double buffer, [warp][2 R].
-template <int R, int WPR>
-__device__ __forceinline__ void team_sums(float (&s1)[R], float (&s2)[R], float* slots, int team) {
-  constexpr int V = 2 * R;
+// Sums a and b over the warp with shared butterflies (the first step leaves each
+// half of the warp with one of them): lanes 0 .. 15 return a's, the others b's.
+__device__ __forceinline__ float warp_sum2(float a, float b) {
   constexpr unsigned kAll = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float v;
-  int mine;
-  if constexpr (R == 2) {
-    const bool up = lane & 16;
-    const float a = (up ? s1[1] : s1[0]) + __shfl_xor_sync(kAll, up ? s1[0] : s1[1], 16);
-    const float b = (up ? s2[1] : s2[0]) + __shfl_xor_sync(kAll, up ? s2[0] : s2[1], 16);
-    v = (lane & 8 ? b : a) + __shfl_xor_sync(kAll, lane & 8 ? a : b, 8);
-    mine = lane >> 3;                     // s1[0], s2[0], s1[1], s2[1]
-  } else {
-    v = (lane & 16 ? s2[0] : s1[0]) + __shfl_xor_sync(kAll, lane & 16 ? s1[0] : s2[0], 16);
-    v += __shfl_xor_sync(kAll, v, 8);
-    mine = lane >> 4;
-  }
+  const bool up = threadIdx.x & 16;
+  float v = (up ? b : a) + __shfl_xor_sync(kAll, up ? a : b, 16);
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  constexpr int kSpread = 32 / V;         // lanes that hold one value
-  if constexpr (WPR == 1) {
-    __syncwarp();                         // the team has read its stages
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      s1[q] = __shfl_sync(kAll, v, 2 * q * kSpread);
-      s2[q] = __shfl_sync(kAll, v, (2 * q + 1) * kSpread);
-    }
-  } else {
-    if (lane % kSpread == 0) slots[warp * V + mine] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(WPR * 32) : "memory");
-    constexpr int kAtOnce = kSpread < WPR ? kSpread : WPR;    // warps' values that lanes load
-    const float* first = slots + (team * WPR + lane / V % kAtOnce) * V + lane % V;
-    v = first[0];
-    if constexpr (WPR > kAtOnce) v += first[kAtOnce * V];
-#pragma unroll
-    for (int o = V; o < V * kAtOnce; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      s1[q] = __shfl_sync(kAll, v, 2 * q);
-      s2[q] = __shfl_sync(kAll, v, 2 * q + 1);
-    }
-  }
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
 }
+
+constexpr int kBwdThreads = 512;
 
 template <class D, class W, int VEC, int C, int WPR>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -364,13 +330,14 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   using T = typename D::T;
   using L = Lanes<VEC>;
   using P = typename L::T;
-  constexpr int kTeams = kBwdThreads / 32 / WPR, TPR = WPR * 32, N = L::N;
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int kWarps = kBwdThreads / 32, kTeams = kWarps / WPR, TPR = WPR * 32, N = L::N;
   constexpr bool kRing = VEC == 8;
-  constexpr int R = kRing && D::kBytes == 2 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[2][kBwdThreads / 32 * 2 * R];
+  __shared__ float2 slots[2][kWarps];     // the warps' sums, in turn by row
   __shared__ uint64_t bars[kTeams * 8];
-  const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  __shared__ float2 stats[kTeams * 8];    // mean and rstd of the stages' rows
+  const int team = threadIdx.x / TPR, t = threadIdx.x % TPR, lane = threadIdx.x & 31;
   if (kRing && threadIdx.x == 0) {
     for (int i = 0; i < kTeams * 8; ++i) tma::mbar_init(&bars[i], 1);
     tma::mbar_init_fence();
@@ -382,35 +349,52 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   const uint32_t row_bytes = (uint32_t)hidden * sizeof(T);
   uint8_t* ring = smem + (size_t)team * stages * 2 * row_bytes;
   uint64_t* full = bars + team * 8;
+  // After a wait that gave up nobody waits, and nothing more is fetched.
   bool dead = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (tma::mbar_try(bar, parity) || dead) return;
+    if (!tma::mbar_wait(bar, parity)) {
+      atomicOr(&g_norm_errors, MOE_DEVERR_TIMEOUT);
+      dead = true;
+    }
+  };
   // The stages are used in turn: `put` and `get` walk through them.
   int put = 0, get = 0, issued = 0;
   uint32_t parity = 0;
+  float next_m = 0.f, next_rs = 0.f;      // the statistics of the row to be loaded next
+  auto load_stats = [&](int k) {
+    if (k < n) {
+      next_m = __ldg(mean + first + k * step);
+      next_rs = __ldg(rstd + first + k * step);
+    }
+  };
+  load_stats(0);
   auto issue = [&] {                      // the next row's copies; by the team's first thread
     const int64_t r = first + issued * step;
     uint8_t* dst = ring + (size_t)put * 2 * row_bytes;
+    stats[team * 8 + put] = make_float2(next_m, next_rs);
     tma::mbar_arrive_expect_tx(&full[put], 2 * row_bytes);
     tma::bulk_load(dst, x + r * ld_x, row_bytes, &full[put]);
     tma::bulk_load(dst + row_bytes, gy + r * ld_gy, row_bytes, &full[put]);
-    ++issued;
+    load_stats(++issued);
     if (++put == stages) put = 0;
   };
-  Unit<D, VEC> nx[R][C], ng[R][C];
+  Unit<D, VEC> nx[kRing ? 1 : C], ng[kRing ? 1 : C];
   auto load = [&](int k) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int h = (c * TPR + t) * VEC;
       if (h < hidden) {
-        nx[0][c].load(x + (first + k * step) * ld_x + h);
-        ng[0][c].load(gy + (first + k * step) * ld_gy + h);
+        nx[c].load(x + (first + k * step) * ld_x + h);
+        ng[c].load(gy + (first + k * step) * ld_gy + h);
       }
     }
   };
-  if (kRing) {
+  if constexpr (kRing) {
     if (t == 0)
       while (issued < stages && issued < n) issue();
-  } else if (n > 0) {
-    load(0);
+  } else {
+    if (n > 0) load(0);
   }
   // With VEC = 8 the weights lie in shared memory (a unit's halves in two planes,
   // free of bank conflicts), else in registers.
@@ -418,11 +402,11 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   const int units = hidden / 8;
   P kept[kRing ? 1 : C][N];
   if constexpr (kRing) {
-    for (int c = threadIdx.x; c < units; c += kBwdThreads) {
+    for (int c = threadIdx.x; c < units; c += blockDim.x) {
       Unit<W, VEC> u;
-      float v[8];
+      float v[VEC];
       u.load_param(w + c * 8);
-      u.widen(reinterpret_cast<float (&)[VEC]>(v));
+      u.widen(v);
       weights[c] = make_float4(v[0], v[1], v[2], v[3]);
       weights[units + c] = make_float4(v[4], v[5], v[6], v[7]);
     }
@@ -447,115 +431,111 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   auto param = [&](int c, P (&p)[N]) {
     if constexpr (kRing) {
       const float4 lo = weights[c * TPR + t], hi = weights[units + c * TPR + t];
-      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      L::pack(reinterpret_cast<const float (&)[VEC]>(v), p);
+      const float v[VEC] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      L::pack(v, p);
     } else {
       p[0] = kept[c][0];
     }
   };
-  float m[R], rs[R];
-  auto stats = [&](int k) {               // (a row past the last has zeros)
+  const float inv = 1.0f / (float)hidden;
+
+  P xh[kRing ? 1 : C][N], av[kRing ? 1 : C][N];      // the row's xhat and grad_y * weight
+  float m, rs, sum;                       // sum: this lane's of the two (warp_sum2)
+  // xhat, grad_y and a of unit c, from the stage `src` or the registers loaded.
+  auto unit = [&](const T* src, int c, P (&xv)[N], P (&gv)[N], P (&a)[N]) {
+    const int h = (c * TPR + t) * VEC;
+    if constexpr (kRing) {
+      nx[0].load_shared(src + h);
+      ng[0].load_shared(src + hidden + h);
+    }
+    P p[N];
+    float v[VEC];
+    param(c, p);
+    nx[kRing ? 0 : c].widen(v);
+    L::pack(v, xv);
+    ng[kRing ? 0 : c].widen(v);
+    L::pack(v, gv);
+    const P sub = L::all(-m), scale = L::all(rs);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      m[q] = k + q < n ? __ldg(mean + first + (k + q) * step) : 0.f;
-      rs[q] = k + q < n ? __ldg(rstd + first + (k + q) * step) : 0.f;
+    for (int i = 0; i < N; ++i) {
+      xv[i] = mul(add(xv[i], sub), scale);
+      a[i] = mul(gv[i], p[i]);
     }
   };
-  stats(0);
-  const float inv = 1.0f / (float)hidden;
-  for (int k = 0; k < n; k += R) {
-    float row_m[R], row_rs[R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      row_m[q] = m[q];
-      row_rs[q] = rs[q];
-    }
-    if (k + R < n) stats(k + R);
+  auto stage = [&](int at) { return reinterpret_cast<const T*>(ring + (size_t)at * 2 * row_bytes); };
+  for (int k = 0; k < n; ++k) {
+    // ---- gather
+    const int at = get;
     if constexpr (kRing) {
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        if (k + q >= n) break;
-        if (!dead && !tma::mbar_wait(&full[get], parity)) {
-          atomicOr(&g_norm_errors, MOE_DEVERR_TIMEOUT);
-          dead = true;
-        }
-        const T* row = reinterpret_cast<const T*>(ring + (size_t)get * 2 * row_bytes);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int h = (c * TPR + t) * VEC;
-          if (h < hidden) {
-            nx[q][c].load_shared(row + h);
-            ng[q][c].load_shared(row + hidden + h);
-          }
-        }
-        if (++get == stages) { get = 0; parity ^= 1u; }
-      }
+      wait(&full[get], parity);
+      const float2 st = stats[team * 8 + get];
+      m = st.x;
+      rs = st.y;
+      if (++get == stages) { get = 0; parity ^= 1u; }
+    } else {
+      m = next_m;
+      rs = next_rs;
+      load_stats(k + 1);
     }
-    P xh[R][C][N];
-    Unit<D, VEC> g_raw[R][C];
-    float s1[R], s2[R];
-    P t1[R], t2[R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) t1[q] = t2[q] = L::all(0.f);
+    P t1 = L::all(0.f), t2 = L::all(0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if ((c * TPR + t) * VEC < hidden) {
-        P p[N];
-        param(c, p);
+        P xv[N], gv[N], a[N];
+        unit(stage(at), c, xv, gv, a);
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          if (k + q >= n) break;
-          const P sub = L::all(-row_m[q]), scale = L::all(row_rs[q]);
-          float v[VEC];
-          P gv[N];
-          nx[q][c].widen(v);
-          L::pack(v, xh[q][c]);
-          g_raw[q][c] = ng[q][c];
-          ng[q][c].widen(v);
-          L::pack(v, gv);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            xh[q][c][i] = mul(add(xh[q][c][i], sub), scale);
-            const P g_xh = mul(gv[i], xh[q][c][i]);
-            dw[c][i] = add(dw[c][i], g_xh);
-            db[c][i] = add(db[c][i], gv[i]);
-            t1[q] = fma(gv[i], p[i], t1[q]);
-            t2[q] = fma(g_xh, p[i], t2[q]);
+        for (int i = 0; i < N; ++i) {
+          dw[c][i] = fma(gv[i], xv[i], dw[c][i]);
+          db[c][i] = add(db[c][i], gv[i]);
+          t1 = add(t1, a[i]);
+          t2 = fma(a[i], xv[i], t2);
+          if constexpr (!kRing) {
+            xh[c][i] = xv[i];
+            av[c][i] = a[i];
           }
         }
       }
     }
-    if (!kRing && k + 1 < n) load(k + 1);
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      s1[q] = L::total(t1[q]);
-      s2[q] = L::total(t2[q]);
+    if constexpr (!kRing) {
+      if (k + 1 < n) load(k + 1);
     }
-    team_sums<R, WPR>(s1, s2, red[k / R & 1], team);
-    if (kRing && t == 0 && !dead)
-      for (int q = 0; q < R && issued < n; ++q) issue();
+    sum = warp_sum2(L::total(t1), L::total(t2));
+    float v = sum;
+    if constexpr (WPR > 1) {
+      if ((lane & 15) == 0)
+        reinterpret_cast<float*>(&slots[k & 1][threadIdx.x >> 5])[lane >> 4] = sum;
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TPR) : "memory");
+      // ---- finish: lanes 0 .. 15 the first sum of the team's warps, the others the second
+      v = reinterpret_cast<const float*>(slots[k & 1] + team * WPR)[(lane & (WPR - 1)) * 2 +
+                                                                   (lane >> 4)];
+#pragma unroll
+      for (int o = WPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    }
+    const float s1 = __shfl_sync(kAll, v, 0) * inv, s2 = __shfl_sync(kAll, v, 16) * inv;
+    // The team has met (a warp alone: met itself), so it has finished the row before: that
+    // row's stage can be refilled.
+    if constexpr (kRing) {
+      if (WPR == 1) __syncwarp();
+      if (t == 0 && !dead && k > 0 && issued < n) issue();
+    }
+    // rstd (a - mean(a) - xhat mean(a xhat))
+    const P scale = L::all(rs), a1 = L::all(-rs * s1), a2 = L::all(-rs * s2);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int h = (c * TPR + t) * VEC;
       if (h < hidden) {
-        P p[N];
-        param(c, p);
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-          if (k + q >= n) break;
-          // rstd (g p - mean(a) - xhat mean(a xhat))
-          const P scale = L::all(row_rs[q]);
-          const P a1 = L::all(-row_rs[q] * (s1[q] * inv)), a2 = L::all(-row_rs[q] * (s2[q] * inv));
-          float v[VEC];
-          P gv[N];
-          g_raw[q][c].widen(v);
-          L::pack(v, gv);
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            gv[i] = fma(xh[q][c][i], a2, fma(mul(gv[i], p[i]), scale, a1));
-          L::unpack(gv, v);
-          Unit<D, VEC>::store(gx + (first + (k + q) * step) * ld_gx + h, v);
+        P xv[N], gv[N], a[N];
+        float out[VEC];
+        if constexpr (kRing) {
+          unit(stage(at), c, xv, gv, a);
+        } else {
+          xv[0] = xh[c][0];
+          a[0] = av[c][0];
         }
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] = fma(xv[i], a2, fma(a[i], scale, a1));
+        L::unpack(a, out);
+        Unit<D, VEC>::store(gx + (first + k * step) * ld_gx + h, out);
       }
     }
   }
@@ -582,7 +562,7 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   }
   if constexpr (kTeams > 1) {             // the teams' shares, in their order
     __syncthreads();
-    for (int h = threadIdx.x; h < 2 * hidden; h += kBwdThreads) {
+    for (int h = threadIdx.x; h < 2 * hidden; h += blockDim.x) {
       const bool bias = h >= hidden;
       const float* v = all + (bias ? kTeams * hidden + h - hidden : h);
       float s = 0.f;
@@ -699,12 +679,17 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
   };
   int rc = MOE_OK;
   const bool vec = eights(hidden, {gy, x, w, gx}, {ld_gy, ld_x, ld_gx});
+  // 4 units a thread where the ring then holds two stages at least of every team (fp32: 2)
+  constexpr int C = D::kBytes == 2 ? 4 : 2, F = 4 / C;
   if (vec && hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 1>, 8, 16);
-  else if (vec && hidden <= 512) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 2>, 8, 8);
-  else if (vec && hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 4>, 8, 4);
-  else if (vec && hidden <= 2048) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 8>, 8, 2);
-  else if (vec && hidden <= 4096) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 16>, 8, 1);
-  else if (vec && hidden <= 8192) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 16>, 8, 1);
+  else if (vec && hidden <= 512) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 1>, 8, 16);
+  else if (vec && hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 8, C, F>, 8, 16 / F);
+  else if (vec && hidden <= 2048)
+    rc = rows_in_registers(norm_bwd_rows<D, W, 8, C, 2 * F>, 8, 8 / F);
+  else if (vec && hidden <= 4096)
+    rc = rows_in_registers(norm_bwd_rows<D, W, 8, C, 4 * F>, 8, 4 / F);
+  else if (vec && hidden <= 8192)
+    rc = rows_in_registers(norm_bwd_rows<D, W, 8, C, 8 * F>, 8, 2 / F);
   else if (hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 1>, 1, 16);
   else if (hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 4>, 1, 4);
   else if (hidden <= 4096) rc = rows_in_registers(norm_bwd_rows<D, W, 1, 8, 16>, 1, 1);
