@@ -81,6 +81,8 @@ class MoeError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libmoe_epilogue.so (built in-tree); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -113,11 +115,28 @@ def ptr(a) -> int | None:
     return a.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """A function that returns torch's current stream's handle (None without a GPU): a small
+    op's launch is short beside a torch.cuda.Stream object's construction (about 3 us)."""
+    import torch
+    if not torch.cuda.is_available():
+        return lambda: None
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(torch.cuda.current_device())
+
+
 def stream_handle(stream) -> int | None:
     """cudaStream_t from None (torch's current stream), a torch stream or an int."""
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -358,8 +358,8 @@ def _ld(t, name):
 def _place(device, stream):
     """Makes `device` (the tensors') and `stream` (None: the device's current one)
     current, so that a call launches there and what it allocates belongs there."""
-    if not (device.type == "cuda" and torch.cuda.is_available()) or \
-            (stream is None and device.index == torch.cuda.current_device()):
+    if device.type != "cuda" or (stream is None and
+                                 device.index == torch.cuda.current_device()):
         return _HERE
     return _other_place(device, stream)
 
