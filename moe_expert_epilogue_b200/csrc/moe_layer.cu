@@ -99,10 +99,10 @@ struct Layer {
 
 constexpr int kLogitTokens = 4;   // tokens per CTA of the logits kernel
 
-// One expert and kLogitTokens tokens per CTA.  The products and their sum are
-// in 64 bits, so that the summation order cannot decide between two experts:
-// a choice depends on the inputs alone.
-template <class D, class R>
+// One expert and kLogitTokens tokens per CTA, VEC elements a thread at a time.
+// The products and their sum are in 64 bits, so that the summation order cannot
+// decide between two experts: a choice depends on the inputs alone.
+template <class D, class R, int VEC>
 __global__ void __launch_bounds__(kThreads)
 layer_logits(Layer a) {
   pdl_prologue();
@@ -113,14 +113,29 @@ layer_logits(Layer a) {
   const auto* w = static_cast<const typename R::T*>(a.router_w) + (int64_t)e * a.hidden;
   const auto* x = static_cast<const typename D::T*>(a.x);
   double acc[kLogitTokens] = {};
-  for (int h = threadIdx.x; h < a.hidden; h += kThreads) {
-    const double wv = load1<R>(w + h);
+#pragma unroll 2
+  for (int h = threadIdx.x * VEC; h < a.hidden; h += kThreads * VEC) {
+    float wv[VEC], xv[kLogitTokens][VEC];
+    if constexpr (VEC == 8) {
+      widen8<R>(load8<R>(w + h), wv);
+#pragma unroll
+      for (int i = 0; i < kLogitTokens; ++i)
+        if (t0 + i < a.tokens) widen8<D>(load8<D>(x + (t0 + i) * a.ld_x + h), xv[i]);
+    } else {
+      wv[0] = load1<R>(w + h);
+#pragma unroll
+      for (int i = 0; i < kLogitTokens; ++i)
+        if (t0 + i < a.tokens) xv[i][0] = load1<D>(x + (t0 + i) * a.ld_x + h);
+    }
 #pragma unroll
     for (int i = 0; i < kLogitTokens; ++i)
-      if (t0 + i < a.tokens) acc[i] += wv * (double)load1<D>(x + (t0 + i) * a.ld_x + h);
+      if (t0 + i < a.tokens)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[i] = fma((double)wv[j], (double)xv[i][j], acc[i]);
   }
 #pragma unroll
   for (int i = 0; i < kLogitTokens; ++i) {
+    if (t0 + i >= a.tokens) break;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(kAll, acc[i], o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][i] = acc[i];
@@ -137,35 +152,56 @@ layer_logits(Layer a) {
 
 // ------------------------------------------------------------ choice
 
-template <int V>
-__device__ void choose_token(const Layer& a, Tables& tb, int t, int lane) {
-  float v[V];
-  const int64_t row = (int64_t)t * a.ld_logits;
-  if (a.logits_dt == MOE_FP32)
-    load_logits<F32, V>(static_cast<const float*>(a.logits) + row, a.E, lane, v);
-  else if (a.logits_dt == MOE_BF16)
-    load_logits<BF16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
-  else
-    load_logits<F16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
-  int id;
-  const float w = route_token<V>(v, a.K, lane, a.softmax, a.normalise, a.scale, &id);
-  int place = 0;             // how many of the token's live experts are lower
-  for (int k = 0; k < a.K; ++k) {
-    const int other = __shfl_sync(kAll, id, k);
-    place += other >= 0 && other < id;
+// The choice of M tokens t, t + step, ... < live by one warp, side by side.
+template <int V, int M>
+__device__ __forceinline__ void choose_tokens(const Layer& a, Tables& tb, int t, int step,
+                                              int live, int lane) {
+  float v[M][V];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int64_t row = (int64_t)min(t + m * step, live - 1) * a.ld_logits;
+    if (a.logits_dt == MOE_FP32)
+      load_logits<F32, V>(static_cast<const float*>(a.logits) + row, a.E, lane, v[m]);
+    else if (a.logits_dt == MOE_BF16)
+      load_logits<BF16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v[m]);
+    else
+      load_logits<F16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v[m]);
   }
-  const unsigned live = __ballot_sync(kAll, id >= 0);
-  if (lane < a.K) {
-    const int slot = t * a.K + lane;
-    tb.expert[slot] = (int16_t)id;
-    tb.weight[slot] = w;
-    if (id >= 0) tb.rank[t * a.K + place] = (uint8_t)lane;
-    if (blockIdx.x == 0) {
-      if (a.topk_weights) a.topk_weights[slot] = w;
-      if (a.topk_ids) a.topk_ids[slot] = id;
+  int id[M];
+  float w[M];
+  route_tokens<V, M>(v, a.K, lane, a.softmax, a.normalise, a.scale, id, w);
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int token = t + m * step;
+    if (token >= live) break;
+    int place = 0;             // how many of the token's live experts are lower
+    for (int k = 0; k < a.K; ++k) {
+      const int other = __shfl_sync(kAll, id[m], k);
+      place += other >= 0 && other < id[m];
     }
+    const unsigned alive = __ballot_sync(kAll, id[m] >= 0);
+    if (lane < a.K) {
+      const int slot = token * a.K + lane;
+      tb.expert[slot] = (int16_t)id[m];
+      tb.weight[slot] = w[m];
+      if (id[m] >= 0) tb.rank[token * a.K + place] = (uint8_t)lane;
+      if (blockIdx.x == 0) {
+        if (a.topk_weights) a.topk_weights[slot] = w[m];
+        if (a.topk_ids) a.topk_ids[slot] = id[m];
+      }
+    }
+    if (lane == 0) tb.live[token] = (uint8_t)__popc(alive);
   }
-  if (lane == 0) tb.live[t] = (uint8_t)__popc(live);
+}
+
+template <int V, int M>
+__device__ __forceinline__ void choose_all(const Layer& a, Tables& tb, int live, int threads) {
+  const int warps = threads / 32, lane = threadIdx.x & 31;
+  for (int t = threadIdx.x >> 5; t < live; t += M * warps) {
+    // (two or more at once only where there are as many)
+    if (M == 1 || t + warps >= live) choose_tokens<V, 1>(a, tb, t, warps, live, lane);
+    else choose_tokens<V, M>(a, tb, t, warps, live, lane);
+  }
 }
 
 // Fills the tables, units of at most `unit_tokens`; all `threads` threads of the
@@ -175,11 +211,9 @@ __device__ void make_tables(const Layer& a, Tables& tb, int unit_tokens, int thr
   const int live = (int)live_tokens(a.valid, a.tokens, a.err);
   for (int e = threadIdx.x; e < a.E; e += threads) tb.count[e] = 0;
   if (threadIdx.x == 0) tb.tokens = live;
-  for (int t = warp; t < live; t += threads / 32) {
-    if (a.E <= 64) choose_token<2>(a, tb, t, lane);
-    else if (a.E <= 256) choose_token<8>(a, tb, t, lane);
-    else choose_token<16>(a, tb, t, lane);
-  }
+  if (a.E <= 64) choose_all<2, 4>(a, tb, live, threads);
+  else if (a.E <= 256) choose_all<8, 4>(a, tb, live, threads);
+  else choose_all<16, 2>(a, tb, live, threads);
   __syncthreads();
   if (warp == 0) {
     // each slot's place among its expert's, in slot order
@@ -608,45 +642,72 @@ __device__ __forceinline__ void load_weights(uint32_t (&r)[4], const WeightAddr<
 }
 
 // This warp's `len` (up to 128) columns of one stage: acc[j] += weights (16
-// rows) x tokens 8 j .. 8 j + 7.  Columns past the unit's last token repeat it;
-// nothing reads their sums.  Shared memory is filled to a multiple of 8 columns:
-// of a last k-step of 16 with 8, the upper half of the fragments is cleared,
-// since what lies there may be anything.
-template <class D, Tiling T, bool SECOND, int NT>
+// rows) x tokens 8 j .. 8 j + 7, for the first CNT of the NT groups of tokens.
+// Columns past the unit's last token repeat it; nothing reads their sums.  The
+// second product's low halves have sums of their own for the stage, so that half
+// as many products wait for one another.
+//   FULL: all 128 columns, without branches.  Else: shared memory is filled to a
+// multiple of 8 columns; of a last k-step of 16 with 8, the upper half of the
+// fragments is cleared, since what lies there may be anything.
+template <class D, Tiling T, bool SECOND, bool FULL, int CNT, int NT>
 __device__ __forceinline__ void multiply(float (&acc)[NT][4], const WeightAddr<T>& w,
                                          uint32_t tokens, const uint32_t (&boff)[NT],
-                                         uint32_t lo_off, int len, int nt, int half, int lane) {
+                                         uint32_t lo_off, int len, int half, int lane) {
+  float low[SECOND ? CNT : 1][4] = {};
 #pragma unroll
   for (int kp = 0; kp < 4; ++kp) {
-    if (kp * 32 >= len) break;
+    if (!FULL && kp * 32 >= len) break;
     uint32_t a0[4], a1[4];
-    const bool both = kp * 32 + 16 < len;
-    const bool cut0 = kp * 32 + 8 >= len, cut1 = kp * 32 + 24 >= len;
+    const bool both = FULL || kp * 32 + 16 < len;
+    const bool cut0 = !FULL && kp * 32 + 8 >= len, cut1 = !FULL && kp * 32 + 24 >= len;
     load_weights<T>(a0, w, half, 2 * kp, lane, len);
     if (both) load_weights<T>(a1, w, half, 2 * kp + 1, lane, len);
     if (cut0) a0[2] = a0[3] = 0;
     if (cut1) a1[2] = a1[3] = 0;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j >= nt) break;
+    for (int j = 0; j < CNT; ++j) {
       uint32_t b[4];
       ldsm4(b, tokens + boff[j] + kp * 64);
       if (cut0) b[1] = 0;
       if (cut1) b[3] = 0;
       mma16816<D>(acc[j], a0, b[0], b[1]);
-      if (SECOND) {
-        uint32_t l[4];
-        ldsm4(l, tokens + boff[j] + lo_off + kp * 64);
-        if (cut0) l[1] = 0;
-        if (cut1) l[3] = 0;
-        mma16816<D>(acc[j], a0, l[0], l[1]);
-        if (both) {
-          mma16816<D>(acc[j], a1, b[2], b[3]);
-          mma16816<D>(acc[j], a1, l[2], l[3]);
-        }
-      } else if (both) {
-        mma16816<D>(acc[j], a1, b[2], b[3]);
+      if (both) mma16816<D>(acc[j], a1, b[2], b[3]);
+      if constexpr (SECOND) {
+        ldsm4(b, tokens + boff[j] + lo_off + kp * 64);
+        if (cut0) b[1] = 0;
+        if (cut1) b[3] = 0;
+        mma16816<D>(low[j], a0, b[0], b[1]);
+        if (both) mma16816<D>(low[j], a1, b[2], b[3]);
       }
+    }
+  }
+  if constexpr (SECOND) {
+#pragma unroll
+    for (int j = 0; j < CNT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] += low[j][i];
+  }
+}
+
+// The same for nt groups of tokens.
+template <class D, Tiling T, bool SECOND, int NT, class... Args>
+__device__ __forceinline__ void multiply_groups(int nt, int len, float (&acc)[NT][4],
+                                                const Args&... args) {
+  if constexpr (NT == 1) {
+    if (len == kSplitCols / 2) multiply<D, T, SECOND, true, 1, NT>(acc, args...);
+    else multiply<D, T, SECOND, false, 1, NT>(acc, args...);
+  } else {
+    const bool full = len == kSplitCols / 2;
+    if (nt == 1) {
+      if (full) multiply<D, T, SECOND, true, 1, NT>(acc, args...);
+      else multiply<D, T, SECOND, false, 1, NT>(acc, args...);
+    } else if (nt == 2) {
+      if (full) multiply<D, T, SECOND, true, 2, NT>(acc, args...);
+      else multiply<D, T, SECOND, false, 2, NT>(acc, args...);
+    } else {
+      // (a fourth group that the unit does not have repeats its last token)
+      if (full) multiply<D, T, SECOND, true, 4, NT>(acc, args...);
+      else multiply<D, T, SECOND, false, 4, NT>(acc, args...);
     }
   }
 }
@@ -727,9 +788,10 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
         WeightAddr<T> w = rel;
         w.row += stage;
         w.row8 += stage;
-        multiply<D, T, SECOND, NT>(acc[s], w,
-                                   stage + S::kWeightBytes + (off + (lane >> 3) * 8) * 2, boff,
-                                   lo_off, min(kSplitCols / 2, len), nt, half, lane);
+        const int cols = min(kSplitCols / 2, len);
+        multiply_groups<D, T, SECOND, NT>(nt, cols, acc[s], w,
+                                          stage + S::kWeightBytes + (off + (lane >> 3) * 8) * 2,
+                                          boff, lo_off, cols, half, lane);
         __syncwarp();
         if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
         slot.next(ring);
@@ -927,8 +989,11 @@ int launch(const Layer& a, cudaStream_t stream) {
   const dim3 grid = a.router_w ? dim3((unsigned)a.E, (unsigned)((a.tokens + kLogitTokens - 1) /
                                                                 kLogitTokens))
                                : dim3(1);
-  launch_kernel_grid(a.router_f32 ? layer_logits<D, F32> : layer_logits<D, D>, grid, kThreads, 0,
-                     stream, a);
+  const bool vec = a.hidden % kVec == 0 && a.ld_x % kVec == 0 && aligned16(a.x) &&
+                   aligned16(a.router_w);
+  launch_kernel_grid(vec ? (a.router_f32 ? layer_logits<D, F32, 8> : layer_logits<D, D, 8>)
+                         : (a.router_f32 ? layer_logits<D, F32, 1> : layer_logits<D, D, 1>),
+                     grid, kThreads, 0, stream, a);
   if (int rc = check_launch()) return rc;
   int sms = 0;
   if (int rc = device_sm_count(&sms)) return rc;
