@@ -67,7 +67,7 @@ struct Tables {
   uint8_t rank[kMaxSlots];       // by slot: k-th place -> k of the token's place-th lowest expert
   uint8_t live[kMaxTokens];      // live slots of a token
   uint8_t token[kMaxSlots];      // by position
-  uint16_t count[kMaxLayerExperts], first[kMaxLayerExperts];
+  uint16_t first[kMaxLayerExperts];
   Unit unit[kMaxUnits];
   int units;
   int most;                      // tokens of the largest unit
@@ -85,6 +85,7 @@ struct Layer {
   int64_t ld_x, ld_logits, ld_shared, ld_residual, ld_out;
   int logits_dt;
   bool router_f32, softmax, normalise;
+  bool eights;           // shared, residual and out in 16-byte pieces
   float scale, limit;
   int32_t* err;
   // workspace
@@ -99,63 +100,108 @@ struct Layer {
 
 constexpr int kLogitTokens = 4;   // tokens per CTA of the logits kernel
 
-// One expert and kLogitTokens tokens per CTA, VEC elements a thread at a time.
-// The products and their sum are in 64 bits, so that the summation order cannot
-// decide between two experts: a choice depends on the inputs alone.
-template <class D, class R, int VEC>
+// Sums of N values over the warp with shared butterflies: each step leaves half
+// of the values to a lane while there are several.  Value i ends up in every lane
+// whose highest bits are i's (from lane 16's bit down), in v[0].
+template <int N>
+__device__ __forceinline__ void warp_sums(double (&v)[N], int lane) {
+  int n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n /= 2;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= n) break;
+        const double keep = lane & o ? v[i + n] : v[i], give = lane & o ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(kAll, give, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(kAll, v[0], o);
+    }
+  }
+}
+
+// EXPERTS experts and kLogitTokens tokens per CTA, VEC elements a thread at a
+// time.  The products and their sums are in 64 bits, so that the summation order
+// cannot decide between two experts: a choice depends on the inputs alone.  What
+// bounds it is the conversion to 64 bits (16 a clock and SM), of which a tile of
+// 4 x 4 needs half a conversion a product.
+template <class D, class R, int VEC, int EXPERTS>
 __global__ void __launch_bounds__(kThreads)
 layer_logits(Layer a) {
   pdl_prologue();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kBarriers) a.barrier[threadIdx.x] = 0;
   if (!a.router_w) return;
-  __shared__ double red[kThreads / 32][kLogitTokens];
-  const int e = blockIdx.x, t0 = blockIdx.y * kLogitTokens;
-  const auto* w = static_cast<const typename R::T*>(a.router_w) + (int64_t)e * a.hidden;
+  constexpr int N = EXPERTS * kLogitTokens;
+  __shared__ double red[kThreads / 32][N];
+  const int e0 = blockIdx.x * EXPERTS, t0 = blockIdx.y * kLogitTokens, lane = threadIdx.x & 31;
+  const auto* w = static_cast<const typename R::T*>(a.router_w);
   const auto* x = static_cast<const typename D::T*>(a.x);
-  double acc[kLogitTokens] = {};
-#pragma unroll 2
+  double acc[N] = {};
   for (int h = threadIdx.x * VEC; h < a.hidden; h += kThreads * VEC) {
-    float wv[VEC], xv[kLogitTokens][VEC];
-    if constexpr (VEC == 8) {
-      widen8<R>(load8<R>(w + h), wv);
+    // (past the last expert or token: the last one again, whose sums nothing reads)
+    float wv[EXPERTS][VEC], xv[kLogitTokens][VEC];
 #pragma unroll
-      for (int i = 0; i < kLogitTokens; ++i)
-        if (t0 + i < a.tokens) widen8<D>(load8<D>(x + (t0 + i) * a.ld_x + h), xv[i]);
-    } else {
-      wv[0] = load1<R>(w + h);
-#pragma unroll
-      for (int i = 0; i < kLogitTokens; ++i)
-        if (t0 + i < a.tokens) xv[i][0] = load1<D>(x + (t0 + i) * a.ld_x + h);
+    for (int i = 0; i < EXPERTS; ++i) {
+      const auto* p = w + (int64_t)min(e0 + i, a.E - 1) * a.hidden + h;
+      if constexpr (VEC == 8) widen8<R>(load8<R>(p), wv[i]);
+      else wv[i][0] = load1<R>(p);
     }
 #pragma unroll
-    for (int i = 0; i < kLogitTokens; ++i)
-      if (t0 + i < a.tokens)
+    for (int i = 0; i < kLogitTokens; ++i) {
+      const auto* p = x + min(t0 + i, a.tokens - 1) * a.ld_x + h;
+      if constexpr (VEC == 8) widen8<D>(load8<D>(p), xv[i]);
+      else xv[i][0] = load1<D>(p);
+    }
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[i] = fma((double)wv[j], (double)xv[i][j], acc[i]);
+    for (int j = 0; j < VEC; ++j) {
+      double wd[EXPERTS];
+#pragma unroll
+      for (int i = 0; i < EXPERTS; ++i) wd[i] = wv[i][j];
+#pragma unroll
+      for (int i = 0; i < kLogitTokens; ++i) {
+        if (EXPERTS == 1 && t0 + i >= a.tokens) break;
+        const double xd = xv[i][j];
+#pragma unroll
+        for (int k = 0; k < EXPERTS; ++k)
+          acc[i * EXPERTS + k] = fma(wd[k], xd, acc[i * EXPERTS + k]);
+      }
+    }
   }
-#pragma unroll
-  for (int i = 0; i < kLogitTokens; ++i) {
-    if (t0 + i >= a.tokens) break;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(kAll, acc[i], o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][i] = acc[i];
-  }
+  warp_sums<N>(acc, lane);
+  constexpr int kSpread = 32 / N;
+  if (lane % kSpread == 0) red[threadIdx.x >> 5][lane / kSpread] = acc[0];
   __syncthreads();
-  const int i = threadIdx.x;
-  if (i < kLogitTokens && t0 + i < a.tokens) {
+  const int i = threadIdx.x / EXPERTS, k = threadIdx.x % EXPERTS;
+  if (i < kLogitTokens && t0 + i < a.tokens && e0 + k < a.E) {
     double s = 0.0;
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) s += red[k][i];
-    a.own_logits[(int64_t)(t0 + i) * a.E + e] = (float)s;
+    for (int r = 0; r < kThreads / 32; ++r) s += red[r][threadIdx.x];
+    a.own_logits[(int64_t)(t0 + i) * a.E + e0 + k] = (float)s;
   }
+}
+
+template <class D, class R>
+void launch_logits(const Layer& a, cudaStream_t stream) {
+  const bool vec = a.hidden % kVec == 0 && a.ld_x % kVec == 0 && aligned16(a.x) &&
+                   aligned16(a.router_w);
+  // four experts a CTA where there are tokens to share their conversion
+  const int experts = a.tokens >= kLogitTokens ? 4 : 1;
+  const dim3 grid = a.router_w ? dim3((unsigned)((a.E + experts - 1) / experts),
+                                      (unsigned)((a.tokens + kLogitTokens - 1) / kLogitTokens))
+                               : dim3(1);
+  const auto k = vec ? (experts == 4 ? layer_logits<D, R, 8, 4> : layer_logits<D, R, 8, 1>)
+                     : (experts == 4 ? layer_logits<D, R, 1, 4> : layer_logits<D, R, 1, 1>);
+  launch_kernel_grid(k, grid, kThreads, 0, stream, a);
 }
 
 // ------------------------------------------------------------ choice
 
 // The choice of M tokens t, t + step, ... < live by one warp, side by side.
 template <int V, int M>
-__device__ __forceinline__ void choose_tokens(const Layer& a, Tables& tb, int t, int step,
-                                              int live, int lane) {
+__device__ __forceinline__ void choose_tokens(const Layer& a, Tables& tb, uint32_t* chosen,
+                                              int t, int step, int live, int lane) {
   float v[M][V];
 #pragma unroll
   for (int m = 0; m < M; ++m) {
@@ -184,7 +230,10 @@ __device__ __forceinline__ void choose_tokens(const Layer& a, Tables& tb, int t,
       const int slot = token * a.K + lane;
       tb.expert[slot] = (int16_t)id[m];
       tb.weight[slot] = w[m];
-      if (id[m] >= 0) tb.rank[token * a.K + place] = (uint8_t)lane;
+      if (id[m] >= 0) {
+        tb.rank[token * a.K + place] = (uint8_t)lane;
+        atomicOr(&chosen[id[m] * (kMaxTokens / 32) + (token >> 5)], 1u << (token & 31));
+      }
       if (blockIdx.x == 0) {
         if (a.topk_weights) a.topk_weights[slot] = w[m];
         if (a.topk_ids) a.topk_ids[slot] = id[m];
@@ -195,77 +244,75 @@ __device__ __forceinline__ void choose_tokens(const Layer& a, Tables& tb, int t,
 }
 
 template <int V, int M>
-__device__ __forceinline__ void choose_all(const Layer& a, Tables& tb, int live, int threads) {
+__device__ __forceinline__ void choose_all(const Layer& a, Tables& tb, uint32_t* chosen, int live,
+                                           int threads) {
   const int warps = threads / 32, lane = threadIdx.x & 31;
   for (int t = threadIdx.x >> 5; t < live; t += M * warps) {
     // (two or more at once only where there are as many)
-    if (M == 1 || t + warps >= live) choose_tokens<V, 1>(a, tb, t, warps, live, lane);
-    else choose_tokens<V, M>(a, tb, t, warps, live, lane);
+    if (M == 1 || t + warps >= live) choose_tokens<V, 1>(a, tb, chosen, t, warps, live, lane);
+    else choose_tokens<V, M>(a, tb, chosen, t, warps, live, lane);
   }
 }
 
 // Fills the tables, units of at most `unit_tokens`; all `threads` threads of the
-// CTA take part.
-__device__ void make_tables(const Layer& a, Tables& tb, int unit_tokens, int threads) {
+// CTA take part.  chosen [E][kMaxTokens / 32] (scratch): the tokens of each expert
+// as bits, from which counts and places follow without an order of writing.
+__device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int unit_tokens,
+                            int threads) {
+  constexpr int kWords = kMaxTokens / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int live = (int)live_tokens(a.valid, a.tokens, a.err);
-  for (int e = threadIdx.x; e < a.E; e += threads) tb.count[e] = 0;
+  for (int i = threadIdx.x; i < a.E * kWords; i += threads) chosen[i] = 0;
   if (threadIdx.x == 0) tb.tokens = live;
-  if (a.E <= 64) choose_all<2, 4>(a, tb, live, threads);
-  else if (a.E <= 256) choose_all<8, 4>(a, tb, live, threads);
-  else choose_all<16, 2>(a, tb, live, threads);
+  __syncthreads();
+  if (a.E <= 64) choose_all<2, 4>(a, tb, chosen, live, threads);
+  else if (a.E <= 256) choose_all<8, 4>(a, tb, chosen, live, threads);
+  else choose_all<16, 2>(a, tb, chosen, live, threads);
   __syncthreads();
   if (warp == 0) {
-    // each slot's place among its expert's, in slot order
-    const int slots = live * a.K;
-    for (int s0 = 0; s0 < slots; s0 += 32) {
-      const int e = s0 + lane < slots ? tb.expert[s0 + lane] : -1;
-      const unsigned peers = __match_any_sync(kAll, e);
-      const int before = e >= 0 ? tb.count[e] : 0;
-      __syncwarp();
-      if (e >= 0) {
-        tb.position[s0 + lane] = (uint16_t)(before + __popc(peers & ((1u << lane) - 1u)));
-        if (lane == 31 - __clz(peers)) tb.count[e] = (uint16_t)(before + __popc(peers));
-      }
-      __syncwarp();
-    }
     // the experts' first positions and units
     int base = 0, units = 0, most = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane, n = e < a.E ? tb.count[e] : 0;
+      const int e = e0 + lane;
+      int n = 0;
+      if (e < a.E) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) n += __popc(chosen[e * kWords + i]);
+      }
       const int u = (n + unit_tokens - 1) / unit_tokens;
       most = max(most, min(n, unit_tokens));
-      int sn = n, su = u;                                   // inclusive prefix sums
+      int sum = n | u << 16;                                // inclusive prefix sums
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int pn = __shfl_up_sync(kAll, sn, o), pu = __shfl_up_sync(kAll, su, o);
-        if (lane >= o) { sn += pn; su += pu; }
+        const int before = __shfl_up_sync(kAll, sum, o);
+        if (lane >= o) sum += before;
       }
       if (e < a.E) {
-        const int first = base + sn - n;
+        const int first = base + (sum & 0xffff) - n;
         tb.first[e] = (uint16_t)first;
         for (int i = 0; i < u; ++i)
-          tb.unit[units + su - u + i] = {(uint16_t)e, (uint16_t)(first + i * unit_tokens),
-                                         (uint16_t)min(unit_tokens, n - i * unit_tokens)};
+          tb.unit[units + (sum >> 16) - u + i] = {(uint16_t)e, (uint16_t)(first + i * unit_tokens),
+                                                  (uint16_t)min(unit_tokens, n - i * unit_tokens)};
       }
-      base += __shfl_sync(kAll, sn, 31);
-      units += __shfl_sync(kAll, su, 31);
+      const int total = __shfl_sync(kAll, sum, 31);
+      base += total & 0xffff;
+      units += total >> 16;
     }
     most = __reduce_max_sync(kAll, most);
     if (lane == 0) {
       tb.units = units;
       tb.most = most;
     }
-    __syncwarp();
-    for (int s = lane; s < slots; s += 32) {
-      const int e = tb.expert[s];
-      if (e >= 0) {
-        const int p = tb.first[e] + tb.position[s];
-        tb.position[s] = (uint16_t)p;
-        tb.order[p] = (uint16_t)s;
-        tb.token[p] = (uint8_t)(s / a.K);
-      }
-    }
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < live * a.K; s += threads) {
+    const int e = tb.expert[s], t = s / a.K;
+    if (e < 0) continue;
+    int p = tb.first[e] + __popc(chosen[e * kWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
+    for (int i = 0; i < t >> 5; ++i) p += __popc(chosen[e * kWords + i]);
+    tb.position[s] = (uint16_t)p;
+    tb.order[p] = (uint16_t)s;
+    tb.token[p] = (uint8_t)t;
   }
   __syncthreads();
 }
@@ -339,6 +386,13 @@ __device__ __forceinline__ float ld_cg(const float* p) {
   return v;
 }
 
+__device__ __forceinline__ void ld_cg4(const float* p, float* v) {
+  asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "l"(p)
+               : "memory");
+}
+
 constexpr int kConsumers = 8, kTokenWarps = 3;                   // and one weight warp
 constexpr int kLayerThreads = (kConsumers + 1 + kTokenWarps) * 32;
 constexpr int kSplitCols = 256;                                  // a block of the axis
@@ -362,6 +416,7 @@ struct Tile {
 constexpr int kRingBytes = (232448 - (int)sizeof(Tables) - 2 * kRedBytes - 256) / 1024 * 1024 - 1024;
 static_assert(kRingBytes / 1024 >= 2 * (32 + 2 * kUnitTokens * (kSplitCols * 2 + 16) / 1024 + 1),
               "two stages at least");
+static_assert(kRingBytes >= kMaxLayerExperts * (kMaxTokens / 32) * 4, "room for make_tables");
 
 struct Ring {
   uint8_t* base;         // 1024-byte aligned
@@ -844,6 +899,56 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
   }
 }
 
+// out = residual + (the rows of a token's experts, ascending, + shared), VEC
+// columns a thread at a time; the loads of four experts' rows are in flight together.
+template <class D, int VEC>
+__device__ __forceinline__ void combine(const Layer& a, const Tables& tb) {
+  const int per_row = a.hidden / VEC, total = tb.tokens * per_row;
+  for (int i = blockIdx.x * (kConsumers * 32) + threadIdx.x; i < total;
+       i += gridDim.x * (kConsumers * 32)) {
+    const int t = i / per_row, c = (i - t * per_row) * VEC;
+    const int live = tb.live[t];
+    float s[VEC] = {};
+    for (int k0 = 0; k0 < live; k0 += 4) {
+      float v[4][VEC];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= live) break;
+        const int slot = t * a.K + tb.rank[t * a.K + k0 + k];
+        const float* y = a.y + (int64_t)tb.position[slot] * a.hidden + c;
+        if constexpr (VEC == 8) {
+          ld_cg4(y, v[k]);
+          ld_cg4(y + 4, v[k] + 4);
+        } else {
+          v[k][0] = ld_cg(y);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= live) break;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s[j] += v[k][j];
+      }
+    }
+    const auto add = [&](const void* base, int64_t ld) {
+      const uint16_t* p = static_cast<const uint16_t*>(base) + t * ld + c;
+      if constexpr (VEC == 8) {
+        float o[8];
+        widen8<D>(load8<D, false>(p), o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = o[j] + s[j];
+      } else {
+        s[0] = load1c<D>(p) + s[0];
+      }
+    };
+    if (a.shared) add(a.shared, a.ld_shared);
+    if (a.residual) add(a.residual, a.ld_residual);      // (before the store: out may be it)
+    uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ld_out + c;
+    if constexpr (VEC == 8) store8<D>(out, s);
+    else store1<D>(out, s[0]);
+  }
+}
+
 template <class D, Tiling T>
 __global__ void __launch_bounds__(kLayerThreads, 1)
 layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMaps maps) {
@@ -852,7 +957,7 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   __shared__ float4 red[2 * kRedBytes / 16];
   __shared__ uint64_t bars[2 * kMaxStages];
   __shared__ int gave_up;
-  extern __shared__ uint8_t ring_mem[];
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     gave_up = 0;
@@ -862,7 +967,11 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
     }
     tma::mbar_init_fence();
   }
-  make_tables(a, tb, S::kTokens, kLayerThreads);
+  pdl_prologue();
+  // (the ring serves as scratch before its first copies)
+  make_tables(a, tb, reinterpret_cast<uint32_t*>(ring_mem), S::kTokens, kLayerThreads);
+  fence_async_proxy();                   // ... by bulk copies
+  __syncthreads();
   const GiveUp g{&gave_up, a.err};
   Ring ring;
   ring.base = ring_mem + ((1024u - (tma::smem_addr(ring_mem) & 1023u)) & 1023u);
@@ -897,23 +1006,8 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
     grid_wait(&a.barrier[1], g);
   }
   consumers_sync();
-  // combine: the chosen experts of a token in ascending order
-  const int64_t total = (int64_t)tb.tokens * a.hidden;
-  for (int64_t i = (int64_t)blockIdx.x * (kConsumers * 32) + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * (kConsumers * 32)) {
-    const int t = (int)(i / a.hidden), c = (int)(i % a.hidden);
-    float s = 0.f;
-    for (int k = 0; k < tb.live[t]; ++k) {
-      const int slot = t * a.K + tb.rank[t * a.K + k];
-      s += ld_cg(a.y + (int64_t)tb.position[slot] * a.hidden + c);
-    }
-    if (a.shared)
-      s += load1<D>(static_cast<const uint16_t*>(a.shared) + t * a.ld_shared + c);
-    // (read before written: out may be residual)
-    if (a.residual)
-      s = load1c<D>(static_cast<const uint16_t*>(a.residual) + t * a.ld_residual + c) + s;
-    store1<D>(static_cast<uint16_t*>(a.out) + t * a.ld_out + c, s);
-  }
+  if (a.eights) combine<D, 8>(a, tb);
+  else combine<D, 1>(a, tb);
 }
 
 // ------------------------------------------------------------ workspace
@@ -975,25 +1069,21 @@ int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t
   cfg.blockDim = dim3(kLayerThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = MOE_PDL;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   (void)cudaLaunchKernelEx(&cfg, layer_experts<D, T>, a, maps);
   return check_launch();
 }
 
 template <class D>
 int launch(const Layer& a, cudaStream_t stream) {
-  const dim3 grid = a.router_w ? dim3((unsigned)a.E, (unsigned)((a.tokens + kLogitTokens - 1) /
-                                                                kLogitTokens))
-                               : dim3(1);
-  const bool vec = a.hidden % kVec == 0 && a.ld_x % kVec == 0 && aligned16(a.x) &&
-                   aligned16(a.router_w);
-  launch_kernel_grid(vec ? (a.router_f32 ? layer_logits<D, F32, 8> : layer_logits<D, D, 8>)
-                         : (a.router_f32 ? layer_logits<D, F32, 1> : layer_logits<D, D, 1>),
-                     grid, kThreads, 0, stream, a);
+  if (a.router_f32) launch_logits<D, F32>(a, stream);
+  else launch_logits<D, D>(a, stream);
   if (int rc = check_launch()) return rc;
   int sms = 0;
   if (int rc = device_sm_count(&sms)) return rc;
@@ -1041,6 +1131,9 @@ int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream) {
   a.h = reinterpret_cast<uint16_t*>(ws + s.h);
   a.y = reinterpret_cast<float*>(ws + s.y);
   a.ld_h = (m.inter + 7) / 8 * 8;
+  a.eights = m.hidden % kVec == 0 && m.ld_out % kVec == 0 && aligned16(m.out) &&
+             (!m.shared || (m.ld_shared % kVec == 0 && aligned16(m.shared))) &&
+             (!m.residual || (m.ld_residual % kVec == 0 && aligned16(m.residual)));
   a.logits = m.router_w ? a.own_logits : m.logits;
   a.logits_dt = m.router_w ? MOE_FP32 : m.logits_dt;
   a.ld_logits = m.router_w ? m.E : m.ld_logits;
