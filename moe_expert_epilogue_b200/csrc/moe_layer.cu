@@ -139,6 +139,7 @@ layer_logits(Layer a) {
   const auto* w = static_cast<const typename R::T*>(a.router_w);
   const auto* x = static_cast<const typename D::T*>(a.x);
   double acc[N] = {};
+#pragma unroll 2
   for (int h = threadIdx.x * VEC; h < a.hidden; h += kThreads * VEC) {
     // (past the last expert or token: the last one again, whose sums nothing reads)
     float wv[EXPERTS][VEC], xv[kLogitTokens][VEC];
@@ -186,8 +187,9 @@ template <class D, class R>
 void launch_logits(const Layer& a, cudaStream_t stream) {
   const bool vec = a.hidden % kVec == 0 && a.ld_x % kVec == 0 && aligned16(a.x) &&
                    aligned16(a.router_w);
-  // four experts a CTA where there are tokens to share their conversion
-  const int experts = a.tokens >= kLogitTokens ? 4 : 1;
+  // four experts a CTA where that leaves a CTA to most of the SMs
+  const int64_t tiles = (int64_t)((a.E + 3) / 4) * ((a.tokens + kLogitTokens - 1) / kLogitTokens);
+  const int experts = tiles >= 128 ? 4 : 1;
   const dim3 grid = a.router_w ? dim3((unsigned)((a.E + experts - 1) / experts),
                                       (unsigned)((a.tokens + kLogitTokens - 1) / kLogitTokens))
                                : dim3(1);
@@ -198,59 +200,55 @@ void launch_logits(const Layer& a, cudaStream_t stream) {
 
 // ------------------------------------------------------------ choice
 
-// The choice of M tokens t, t + step, ... < live by one warp, side by side.
-template <int V, int M>
-__device__ __forceinline__ void choose_tokens(const Layer& a, Tables& tb, uint32_t* chosen,
-                                              int t, int step, int live, int lane) {
-  float v[M][V];
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const int64_t row = (int64_t)min(t + m * step, live - 1) * a.ld_logits;
-    if (a.logits_dt == MOE_FP32)
-      load_logits<F32, V>(static_cast<const float*>(a.logits) + row, a.E, lane, v[m]);
-    else if (a.logits_dt == MOE_BF16)
-      load_logits<BF16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v[m]);
-    else
-      load_logits<F16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v[m]);
-  }
-  int id[M];
-  float w[M];
-  route_tokens<V, M>(v, a.K, lane, a.softmax, a.normalise, a.scale, id, w);
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const int token = t + m * step;
-    if (token >= live) break;
-    int place = 0;             // how many of the token's live experts are lower
-    for (int k = 0; k < a.K; ++k) {
-      const int other = __shfl_sync(kAll, id[m], k);
-      place += other >= 0 && other < id[m];
-    }
-    const unsigned alive = __ballot_sync(kAll, id[m] >= 0);
-    if (lane < a.K) {
-      const int slot = token * a.K + lane;
-      tb.expert[slot] = (int16_t)id[m];
-      tb.weight[slot] = w[m];
-      if (id[m] >= 0) {
-        tb.rank[token * a.K + place] = (uint8_t)lane;
-        atomicOr(&chosen[id[m] * (kMaxTokens / 32) + (token >> 5)], 1u << (token & 31));
-      }
-      if (blockIdx.x == 0) {
-        if (a.topk_weights) a.topk_weights[slot] = w[m];
-        if (a.topk_ids) a.topk_ids[slot] = id[m];
-      }
-    }
-    if (lane == 0) tb.live[token] = (uint8_t)__popc(alive);
-  }
+// The logits of token t, experts [lane * V, lane * V + V).
+template <int V>
+__device__ __forceinline__ void token_logits(const Layer& a, int t, int lane, float (&v)[V]) {
+  const int64_t row = (int64_t)t * a.ld_logits;
+  if (a.logits_dt == MOE_FP32)
+    load_logits<F32, V>(static_cast<const float*>(a.logits) + row, a.E, lane, v);
+  else if (a.logits_dt == MOE_BF16)
+    load_logits<BF16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
+  else
+    load_logits<F16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
 }
 
-template <int V, int M>
-__device__ __forceinline__ void choose_all(const Layer& a, Tables& tb, uint32_t* chosen, int live,
-                                           int threads) {
+// The choices of all live tokens, a warp per token, the next one's logits loaded
+// ahead.  (Several tokens side by side took longer: most of a call's time here is
+// the first fetch of the instructions.)
+template <int V>
+__device__ __forceinline__ void choose(const Layer& a, Tables& tb, uint32_t* chosen, int live,
+                                       int threads) {
   const int warps = threads / 32, lane = threadIdx.x & 31;
-  for (int t = threadIdx.x >> 5; t < live; t += M * warps) {
-    // (two or more at once only where there are as many)
-    if (M == 1 || t + warps >= live) choose_tokens<V, 1>(a, tb, chosen, t, warps, live, lane);
-    else choose_tokens<V, M>(a, tb, chosen, t, warps, live, lane);
+  int t = threadIdx.x >> 5;
+  float next[V];
+  if (t < live) token_logits<V>(a, t, lane, next);
+  for (; t < live; t += warps) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = next[i];
+    if (t + warps < live) token_logits<V>(a, t + warps, lane, next);
+    int id;
+    const float w = route_token<V>(v, a.K, lane, a.softmax, a.normalise, a.scale, &id);
+    int place = 0;             // how many of the token's live experts are lower
+    for (int k = 0; k < a.K; ++k) {
+      const int other = __shfl_sync(kAll, id, k);
+      place += other >= 0 && other < id;
+    }
+    const unsigned alive = __ballot_sync(kAll, id >= 0);
+    if (lane < a.K) {
+      const int slot = t * a.K + lane;
+      tb.expert[slot] = (int16_t)id;
+      tb.weight[slot] = w;
+      if (id >= 0) {
+        tb.rank[t * a.K + place] = (uint8_t)lane;
+        atomicOr(&chosen[id * (kMaxTokens / 32) + (t >> 5)], 1u << (t & 31));
+      }
+      if (blockIdx.x == 0) {
+        if (a.topk_weights) a.topk_weights[slot] = w;
+        if (a.topk_ids) a.topk_ids[slot] = id;
+      }
+    }
+    if (lane == 0) tb.live[t] = (uint8_t)__popc(alive);
   }
 }
 
@@ -265,9 +263,9 @@ __device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int un
   for (int i = threadIdx.x; i < a.E * kWords; i += threads) chosen[i] = 0;
   if (threadIdx.x == 0) tb.tokens = live;
   __syncthreads();
-  if (a.E <= 64) choose_all<2, 4>(a, tb, chosen, live, threads);
-  else if (a.E <= 256) choose_all<8, 4>(a, tb, chosen, live, threads);
-  else choose_all<16, 2>(a, tb, chosen, live, threads);
+  if (a.E <= 64) choose<2>(a, tb, chosen, live, threads);
+  else if (a.E <= 256) choose<8>(a, tb, chosen, live, threads);
+  else choose<16>(a, tb, chosen, live, threads);
   __syncthreads();
   if (warp == 0) {
     // the experts' first positions and units

@@ -61,64 +61,54 @@ __device__ __forceinline__ float chosen_score(bool softmax, float v, float top) 
   return 1.0f / (1.0f + expf(-v));
 }
 
-// The K choices of M tokens from their logits, side by side (lane i holds experts
-// i * V .. i * V + V - 1 in v[m], -inf past the last).  Lane k gets the weight of
-// the k-th choice and its expert (-1 and 0 where nothing is left, or k >= K).
-template <int V, int M>
-__device__ __forceinline__ void route_tokens(const float (&v)[M][V], int K, int lane,
-                                             bool softmax, bool normalise, float scale,
-                                             int (&id)[M], float (&w)[M]) {
-  uint32_t key[M][V];
-  float mine[M];           // lane k: logit of the k-th choice
+// The K choices of one token from its logits (lane i holds experts i * V ..
+// i * V + V - 1 in v, -inf past the last).  Lane k returns the weight of the
+// k-th choice and its expert in *id (0 and -1 where nothing is left, or k >= K).
+// A choice waits for the one before: the chain of a round is the lanes' maximum,
+// the vote on who holds it, and the removal, without branches.
+template <int V>
+__device__ __forceinline__ float route_token(const float (&v)[V], int K, int lane, bool softmax,
+                                             bool normalise, float scale, int* id_out) {
+  uint32_t key[V];
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    mine[m] = -kInf;
-    id[m] = -1;
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[m][i] = order_key(v[m][i]);
-  }
+  for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
+  float mine = -kInf;      // lane k: logit and expert of the k-th choice
+  int id = -1;
   for (int k = 0; k < K; ++k) {
+    uint32_t best = 0;
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      uint32_t best = 0;
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    if (top == 0) break;
+    // the lowest lane, and in it the lowest expert, that holds the largest key
+    const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    bool here = lane == src;
+    int expert = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) best = max(best, key[m][i]);
-      const uint32_t top = __reduce_max_sync(kAll, best);
-      if (M == 1 && top == 0) { k = K; break; }
-      // the lowest lane, and in it the lowest expert, that holds the largest key
-      const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
-      int at = 0;
-      if (lane == src) {
-#pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-          if (key[m][i] == top) at = i;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i == at) key[m][i] = 0;
-      }
-      at = __shfl_sync(kAll, at, src);
-      if (lane == k && top != 0) {
-        mine[m] = key_value(top);
-        id[m] = src * V + at;
-      }
+    for (int i = 0; i < V; ++i) {
+      const bool hit = here && key[i] == top;
+      key[i] = hit ? 0u : key[i];
+      expert = hit ? lane * V + i : expert;
+      here = here && !hit;
     }
+    expert = __shfl_sync(kAll, expert, src);
+    mine = lane == k ? key_value(top) : mine;
+    id = lane == k ? expert : id;
   }
+  const float top = __shfl_sync(kAll, mine, 0);   // the row's largest logit
+  float w = id >= 0 ? chosen_score(softmax, mine, top) : 0.0f;
+  if (softmax && !normalise) {
+    float s = 0.f;
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const float top = __shfl_sync(kAll, mine[m], 0);   // the row's largest logit
-    float x = id[m] >= 0 ? chosen_score(softmax, mine[m], top) : 0.0f;
-    if (softmax && !normalise) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) s += v[m][i] == -kInf ? 0.0f : expf(v[m][i] - top);
-      x = x / warp_sum(s);
-    } else if (normalise) {
-      x = x / warp_sum(x);
-    } else if (id[m] >= 0) {
-      x = 1.0f / (1.0f + expf(-mine[m]));
-    }
-    w[m] = id[m] >= 0 ? x * scale : 0.0f;
+    for (int i = 0; i < V; ++i) s += v[i] == -kInf ? 0.0f : expf(v[i] - top);
+    w = w / warp_sum(s);
+  } else if (normalise) {
+    w = w / warp_sum(w);
+  } else if (id >= 0) {
+    w = 1.0f / (1.0f + expf(-mine));
   }
+  *id_out = id;
+  return id >= 0 ? w * scale : 0.0f;
 }
 
 }  // namespace moe

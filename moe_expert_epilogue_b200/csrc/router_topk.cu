@@ -35,13 +35,13 @@ router_fwd(const typename D::T* __restrict__ logits, float* __restrict__ weights
   const int64_t n = live_tokens(valid, tokens, err);
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < n; t += step) {
-    float v[1][V], w[1];
-    int id[1];
-    load_logits<D, V>(logits + t * ld, E, lane, v[0]);
-    route_tokens<V, 1>(v, K, lane, softmax, normalise, scale, id, w);
+    float v[V];
+    int id;
+    load_logits<D, V>(logits + t * ld, E, lane, v);
+    const float w = route_token<V>(v, K, lane, softmax, normalise, scale, &id);
     if (lane < K) {
-      weights[t * K + lane] = w[0];
-      ids[t * K + lane] = id[0];
+      weights[t * K + lane] = w;
+      ids[t * K + lane] = id;
     }
   }
 }
