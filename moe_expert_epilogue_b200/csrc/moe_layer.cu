@@ -21,18 +21,19 @@
 // producer waits for nothing but free stages: while the slowest CTA finishes the
 // first product, the others' rings fill with the second's weights.
 //
-// The summation order is the same however a product is tiled: the axis is cut
-// into blocks of 256, block c's halves of 128 are accumulated in order into the
-// partial sums (c mod 4, half), and these eight are added in a fixed tree.
-//   kWide   tiles of 64 rows by 256 columns: 2-D tensor copies of 64 columns
-//           (128-byte swizzle); four warps share a block half, each keeping the
-//           four block classes of its 16 rows in registers
+// The summation order is the same however a product is tiled: a block of 256
+// columns of the axis is cut into eight slices of 32, one to a consumer warp,
+// which adds its slices up block after block; the eight sums are added in a fixed
+// tree.  No two warps read the same columns of the tokens.
+//   kWide   tiles of 64 rows by 256 columns: 3-D tensor copies of 64 columns
+//           (128-byte swizzle)
 //   kNarrow tiles of 16 rows by 1024 columns, up to 8 tokens a unit: one bulk copy
-//           of 2 KB a row; each warp has one of the eight partial sums
+//           of 2 KB a row
 //   kAny    as kNarrow where rows start off 16-byte boundaries: the copies take
 //           the 16-byte words around a row, and the consumers shift
 // Row copies of 512 bytes instead of kWide's boxes were bound by their number:
-// halving their bytes changed nothing.
+// halving their bytes changed nothing.  Four warps to a slice of 128 columns, each
+// with a quarter of the rows, were bound by shared memory in the second product.
 #include <cuda.h>
 #include <math.h>
 
@@ -229,20 +230,12 @@ __device__ __forceinline__ void choose(const Layer& a, Tables& tb, uint32_t* cho
     if (t + warps < live) token_logits<V>(a, t + warps, lane, next);
     int id;
     const float w = route_token<V>(v, a.K, lane, a.softmax, a.normalise, a.scale, &id);
-    int place = 0;             // how many of the token's live experts are lower
-    for (int k = 0; k < a.K; ++k) {
-      const int other = __shfl_sync(kAll, id, k);
-      place += other >= 0 && other < id;
-    }
     const unsigned alive = __ballot_sync(kAll, id >= 0);
     if (lane < a.K) {
       const int slot = t * a.K + lane;
       tb.expert[slot] = (int16_t)id;
       tb.weight[slot] = w;
-      if (id >= 0) {
-        tb.rank[t * a.K + place] = (uint8_t)lane;
-        atomicOr(&chosen[id * (kMaxTokens / 32) + (t >> 5)], 1u << (t & 31));
-      }
+      if (id >= 0) atomicOr(&chosen[id * (kMaxTokens / 32) + (t >> 5)], 1u << (t & 31));
       if (blockIdx.x == 0) {
         if (a.topk_weights) a.topk_weights[slot] = w;
         if (a.topk_ids) a.topk_ids[slot] = id;
@@ -306,6 +299,12 @@ __device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int un
   for (int s = threadIdx.x; s < live * a.K; s += threads) {
     const int e = tb.expert[s], t = s / a.K;
     if (e < 0) continue;
+    int place = 0;             // how many of the token's live experts are lower
+    for (int k = 0; k < a.K; ++k) {
+      const int other = tb.expert[t * a.K + k];
+      place += other >= 0 && other < e;
+    }
+    tb.rank[t * a.K + place] = (uint8_t)(s - t * a.K);
     int p = tb.first[e] + __popc(chosen[e * kWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
     for (int i = 0; i < t >> 5; ++i) p += __popc(chosen[e * kWords + i]);
     tb.position[s] = (uint16_t)p;
@@ -394,8 +393,9 @@ __device__ __forceinline__ void ld_cg4(const float* p, float* v) {
 constexpr int kConsumers = 8, kTokenWarps = 3;                   // and one weight warp
 constexpr int kLayerThreads = (kConsumers + 1 + kTokenWarps) * 32;
 constexpr int kSplitCols = 256;                                  // a block of the axis
+constexpr int kSlice = kSplitCols / kConsumers;                  // and a warp's part of it
+static_assert(kSlice == 32, "two k-steps");
 constexpr int kMaxStages = 8;
-constexpr int kRedBytes = 4 * 4 * 32 * 16;                       // one buffer of partial sums
 
 enum Tiling { kWide, kNarrow, kAny };
 
@@ -408,13 +408,18 @@ struct Tile {
   static constexpr int kPitch = T == kAny ? kCols * 2 + 32 : kCols * 2 + 16;   // not of kWide
   static constexpr int kWeightBytes = T == kWide ? kRows * kCols * 2 : kRows * kPitch;
   static constexpr int kTokens = T == kWide ? kUnitTokens : kNarrowTokens;
+  // one buffer of the warps' sums; the ring: stages of weights, then up to 2 * most token rows
+  static constexpr int kRed = kConsumers * (kRows / 16) * 32 * 16;
+  static constexpr int kRing = (232448 - (int)sizeof(Tables) - 512 - 2 * kRed - 1024) / 1024 * 1024;
 };
 
-// The ring: stages of weights, then up to 2 * most token rows.
-constexpr int kRingBytes = (232448 - (int)sizeof(Tables) - 2 * kRedBytes - 256) / 1024 * 1024 - 1024;
-static_assert(kRingBytes / 1024 >= 2 * (32 + 2 * kUnitTokens * (kSplitCols * 2 + 16) / 1024 + 1),
+static_assert(Tile<kWide>::kRing >= 2 * (Tile<kWide>::kWeightBytes +
+                                         2 * kUnitTokens * Tile<kWide>::kTokenPitch + 1023) &&
+                  Tile<kAny>::kRing >= 2 * (Tile<kAny>::kWeightBytes +
+                                            2 * kNarrowTokens * Tile<kAny>::kTokenPitch + 1023),
               "two stages at least");
-static_assert(kRingBytes >= kMaxLayerExperts * (kMaxTokens / 32) * 4, "room for make_tables");
+static_assert(Tile<kWide>::kRing >= kMaxLayerExperts * (kMaxTokens / 32) * 4,
+              "room for make_tables' scratch");
 
 struct Ring {
   uint8_t* base;         // 1024-byte aligned
@@ -669,99 +674,91 @@ __device__ __forceinline__ uint32_t lds_pair(uint32_t addr, int left) {
   return left >= 2 ? v : left == 1 ? v & 0xffffu : 0u;
 }
 
-// Where a warp's 16 rows of weights lie in a stage.
+// Where 16 rows of weights lie in a stage, for this lane.
 template <Tiling T>
 struct WeightAddr {
   uint32_t row;           // kWide, kNarrow: this lane's ldmatrix row; kAny: row g
   uint32_t row8;          // kAny: row g + 8
 };
 
-// The fragment of k-step ks (16 columns) of this warp's 128.
+// The fragments of 16 rows and the 16 columns from `col` on (of which `left` are
+// there) of a stage.
 template <Tiling T>
-__device__ __forceinline__ void load_weights(uint32_t (&r)[4], const WeightAddr<T>& w, int half,
-                                             int ks, int lane, int len) {
+__device__ __forceinline__ void load_weights(uint32_t (&r)[4], const WeightAddr<T>& w, int col,
+                                             int lane, int left) {
   if constexpr (T == kWide) {
-    const int piece = (ks & 3) * 2 + (lane >> 4);
-    ldsm4(r, w.row + (half * 2 + (ks >> 2)) * 8192 + ((piece ^ (lane & 7)) * 16));
+    const int piece = (col >> 3 & 7) + (lane >> 4);
+    ldsm4(r, w.row + (col >> 6) * 8192 + ((piece ^ (lane & 7)) * 16));
   } else if constexpr (T == kNarrow) {
-    ldsm4(r, w.row + ks * 32);
+    ldsm4(r, w.row + col * 2);
   } else {
-    const int c = ks * 16 + (lane & 3) * 2;
-    r[0] = lds_pair(w.row + c * 2, len - c);
-    r[1] = lds_pair(w.row8 + c * 2, len - c);
-    r[2] = lds_pair(w.row + c * 2 + 16, len - c - 8);
-    r[3] = lds_pair(w.row8 + c * 2 + 16, len - c - 8);
+    const int c = (lane & 3) * 2;
+    const uint32_t at = (col + c) * 2;
+    r[0] = lds_pair(w.row + at, left - c);
+    r[1] = lds_pair(w.row8 + at, left - c);
+    r[2] = lds_pair(w.row + at + 16, left - c - 8);
+    r[3] = lds_pair(w.row8 + at + 16, left - c - 8);
   }
 }
 
-// This warp's `len` (up to 128) columns of one stage: acc[j] += weights (16
-// rows) x tokens 8 j .. 8 j + 7, for the first CNT of the NT groups of tokens.
-// Columns past the unit's last token repeat it; nothing reads their sums.  The
-// second product's low halves have sums of their own for the stage, so that half
-// as many products wait for one another.
-//   FULL: all 128 columns, without branches.  Else: shared memory is filled to a
-// multiple of 8 columns; of a last k-step of 16 with 8, the upper half of the
-// fragments is cleared, since what lies there may be anything.
-template <class D, Tiling T, bool SECOND, bool FULL, int CNT, int NT>
-__device__ __forceinline__ void multiply(float (&acc)[NT][4], const WeightAddr<T>& w,
+// A slice of a stage: the 32 columns from `col` on, of which `left` are there:
+// acc[m][j] += weights (16-row group m) x tokens 8 j .. 8 j + 7, for the first CNT
+// groups of tokens.  Columns past the unit's last token repeat it; nothing reads
+// their sums.
+//   FULL: all 32, without branches.  Else: shared memory is filled to a multiple
+// of 8 columns; of a last k-step of 16 with 8, the upper half of the fragments is
+// cleared, since what lies there may be anything.
+template <class D, Tiling T, bool SECOND, bool FULL, int CNT, int M, int NT>
+__device__ __forceinline__ void multiply(float (&acc)[M][NT][4], const WeightAddr<T> (&w)[M],
                                          uint32_t tokens, const uint32_t (&boff)[NT],
-                                         uint32_t lo_off, int len, int half, int lane) {
-  float low[SECOND ? CNT : 1][4] = {};
+                                         uint32_t lo_off, int col, int left, int lane) {
+  if (!FULL && left <= 0) return;
+  const bool both = FULL || left > 16;
+  const bool cut0 = !FULL && left <= 8, cut1 = !FULL && left <= 24;
+  uint32_t b[CNT][SECOND ? 2 : 1][4];
 #pragma unroll
-  for (int kp = 0; kp < 4; ++kp) {
-    if (!FULL && kp * 32 >= len) break;
+  for (int j = 0; j < CNT; ++j) {
+#pragma unroll
+    for (int h = 0; h < (SECOND ? 2 : 1); ++h) {
+      ldsm4(b[j][h], tokens + boff[j] + h * lo_off + col * 2);
+      if (cut0) b[j][h][1] = 0;
+      if (cut1) b[j][h][3] = 0;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
     uint32_t a0[4], a1[4];
-    const bool both = FULL || kp * 32 + 16 < len;
-    const bool cut0 = !FULL && kp * 32 + 8 >= len, cut1 = !FULL && kp * 32 + 24 >= len;
-    load_weights<T>(a0, w, half, 2 * kp, lane, len);
-    if (both) load_weights<T>(a1, w, half, 2 * kp + 1, lane, len);
+    load_weights<T>(a0, w[m], col, lane, left);
+    if (both) load_weights<T>(a1, w[m], col + 16, lane, left - 16);
     if (cut0) a0[2] = a0[3] = 0;
     if (cut1) a1[2] = a1[3] = 0;
 #pragma unroll
-    for (int j = 0; j < CNT; ++j) {
-      uint32_t b[4];
-      ldsm4(b, tokens + boff[j] + kp * 64);
-      if (cut0) b[1] = 0;
-      if (cut1) b[3] = 0;
-      mma16816<D>(acc[j], a0, b[0], b[1]);
-      if (both) mma16816<D>(acc[j], a1, b[2], b[3]);
-      if constexpr (SECOND) {
-        ldsm4(b, tokens + boff[j] + lo_off + kp * 64);
-        if (cut0) b[1] = 0;
-        if (cut1) b[3] = 0;
-        mma16816<D>(low[j], a0, b[0], b[1]);
-        if (both) mma16816<D>(low[j], a1, b[2], b[3]);
-      }
+    for (int h = 0; h < (SECOND ? 2 : 1); ++h)
+#pragma unroll
+      for (int j = 0; j < CNT; ++j) mma16816<D>(acc[m][j], a0, b[j][h][0], b[j][h][1]);
+    if (both) {
+#pragma unroll
+      for (int h = 0; h < (SECOND ? 2 : 1); ++h)
+#pragma unroll
+        for (int j = 0; j < CNT; ++j) mma16816<D>(acc[m][j], a1, b[j][h][2], b[j][h][3]);
     }
-  }
-  if constexpr (SECOND) {
-#pragma unroll
-    for (int j = 0; j < CNT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] += low[j][i];
   }
 }
 
-// The same for nt groups of tokens.
-template <class D, Tiling T, bool SECOND, int NT, class... Args>
-__device__ __forceinline__ void multiply_groups(int nt, int len, float (&acc)[NT][4],
-                                                const Args&... args) {
-  if constexpr (NT == 1) {
-    if (len == kSplitCols / 2) multiply<D, T, SECOND, true, 1, NT>(acc, args...);
-    else multiply<D, T, SECOND, false, 1, NT>(acc, args...);
+// This warp's slices of a stage of `len` columns.
+template <class D, Tiling T, bool SECOND, int CNT, int M, int NT>
+__device__ __forceinline__ void multiply_stage(float (&acc)[M][NT][4], const WeightAddr<T> (&w)[M],
+                                               uint32_t tokens, const uint32_t (&boff)[NT],
+                                               uint32_t lo_off, int len, int warp, int lane) {
+  const int col = warp * kSlice;
+  if (len == Tile<T>::kCols) {
+#pragma unroll
+    for (int c = 0; c < Tile<T>::kCols; c += kSplitCols)
+      multiply<D, T, SECOND, true, CNT>(acc, w, tokens, boff, lo_off, c + col, kSlice, lane);
   } else {
-    const bool full = len == kSplitCols / 2;
-    if (nt == 1) {
-      if (full) multiply<D, T, SECOND, true, 1, NT>(acc, args...);
-      else multiply<D, T, SECOND, false, 1, NT>(acc, args...);
-    } else if (nt == 2) {
-      if (full) multiply<D, T, SECOND, true, 2, NT>(acc, args...);
-      else multiply<D, T, SECOND, false, 2, NT>(acc, args...);
-    } else {
-      // (a fourth group that the unit does not have repeats its last token)
-      if (full) multiply<D, T, SECOND, true, 4, NT>(acc, args...);
-      else multiply<D, T, SECOND, false, 4, NT>(acc, args...);
-    }
+    for (int c = 0; c < len; c += kSplitCols)
+      multiply<D, T, SECOND, false, CNT>(acc, w, tokens, boff, lo_off, c + col, len - c - col,
+                                         lane);
   }
 }
 
@@ -799,13 +796,9 @@ template <class D, Tiling T, bool SECOND>
 __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const Ring& ring,
                                         Slot& slot, float4* red, int& buffer, const GiveUp& g) {
   using S = Tile<T>;
-  constexpr bool WIDE = T == kWide;
-  constexpr int NS = WIDE ? 4 : 1, NT = WIDE ? 4 : 1;
+  constexpr int M = S::kRows / 16, NT = S::kTokens / 8;      // groups of rows, of tokens
   const Product p = make_product<T, SECOND>(a, tb);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int half = warp >> 2, quarter = warp & 3;
-  const int group = WIDE ? quarter : 0;                       // 16-row group of the tile
-  const int off = (WIDE ? 0 : quarter * kSplitCols) + half * (kSplitCols / 2);
   const uint32_t ring_base = tma::smem_addr(ring.base);
   for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
     const Unit u = tb.unit[item / p.tiles];
@@ -815,85 +808,77 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
 #pragma unroll
     for (int j = 0; j < NT; ++j) boff[j] = min(j * 8 + (lane & 7), u.count - 1) * S::kTokenPitch;
     const uint32_t lo_off = u.count * S::kTokenPitch;
-    WeightAddr<T> rel;                                        // within the stage
-    if (T == kWide) {
-      // gate rows 0 .. 31 and up rows 32 .. 63 of the first product's boxes
-      rel.row = (SECOND ? group * 16 + (lane & 15)
-                        : group * 8 + (lane & 7) + (lane & 8) * 4) * 128;
-    } else if (T == kNarrow) {
-      rel.row = (lane & 15) * S::kPitch + (off + (lane >> 4) * 8) * 2;
-    } else {
-      const int r = lane >> 2;
-      const auto lo = reinterpret_cast<uintptr_t>(weight_row<SECOND>(a, u.expert, tile, r));
-      const auto hi = reinterpret_cast<uintptr_t>(weight_row<SECOND>(a, u.expert, tile, r + 8));
-      rel.row = r * S::kPitch + off * 2 + (uint32_t)(lo & 15);
-      rel.row8 = (r + 8) * S::kPitch + off * 2 + (uint32_t)(hi & 15);
-    }
-    float acc[NS][NT][4] = {};
-    for (int c0 = 0; c0 < p.chunks; c0 += NS) {
+    WeightAddr<T> rel[M];                                     // within the stage
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        if (c0 + s >= p.chunks) break;
-        const int len = min(S::kCols, p.axis - (c0 + s) * S::kCols) - off;
-        const uint32_t stage = ring_base + slot.at * ring.stage_bytes;
-        wait_phase(&ring.full[slot.at], slot.parity, g);
-        __syncwarp();
-        WeightAddr<T> w = rel;
-        w.row += stage;
-        w.row8 += stage;
-        const int cols = min(kSplitCols / 2, len);
-        multiply_groups<D, T, SECOND, NT>(nt, cols, acc[s], w,
-                                          stage + S::kWeightBytes + (off + (lane >> 3) * 8) * 2,
-                                          boff, lo_off, cols, half, lane);
-        __syncwarp();
-        if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
-        slot.next(ring);
+    for (int m = 0; m < M; ++m) {
+      if (T == kWide) {
+        // gate rows 0 .. 31 and up rows 32 .. 63 of the first product's boxes
+        rel[m].row = (SECOND ? m * 16 + (lane & 15) : m * 8 + (lane & 7) + (lane & 8) * 4) * 128;
+      } else if (T == kNarrow) {
+        rel[m].row = (lane & 15) * S::kPitch + (lane >> 4) * 16;
+      } else {
+        const int r = lane >> 2;
+        const auto lo = reinterpret_cast<uintptr_t>(weight_row<SECOND>(a, u.expert, tile, r));
+        const auto hi = reinterpret_cast<uintptr_t>(weight_row<SECOND>(a, u.expert, tile, r + 8));
+        rel[m].row = r * S::kPitch + (uint32_t)(lo & 15);
+        rel[m].row8 = (r + 8) * S::kPitch + (uint32_t)(hi & 15);
       }
     }
-    // the eight partial sums, in one order: ((0 + 1) + (2 + 3)) of each half, then the halves
-    float4* r = red + buffer * (kRedBytes / 16);
-    if constexpr (WIDE) {
-      float sum[NT][4];
+    float acc[M][NT][4] = {};
+    for (int c = 0; c < p.chunks; ++c) {
+      const int len = min(S::kCols, p.axis - c * S::kCols);
+      const uint32_t stage = ring_base + slot.at * ring.stage_bytes;
+      wait_phase(&ring.full[slot.at], slot.parity, g);
+      __syncwarp();
+      WeightAddr<T> w[M];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sum[j][i] = (acc[0][j][i] + acc[1][j][i]) + (acc[2][j][i] + acc[3][j][i]);
-        if (half == 1 && j < nt)
-          r[(group * 4 + j) * 32 + lane] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
+      for (int m = 0; m < M; ++m) {
+        w[m].row = rel[m].row + stage;
+        w[m].row8 = rel[m].row8 + stage;
       }
+      const uint32_t tokens = stage + S::kWeightBytes + (lane >> 3) * 16;
+      // (a third group of tokens goes with a fourth, which repeats the last token)
+      if (NT == 1 || nt == 1)
+        multiply_stage<D, T, SECOND, 1>(acc, w, tokens, boff, lo_off, len, warp, lane);
+      else if (nt == 2)
+        multiply_stage<D, T, SECOND, NT < 2 ? 1 : 2>(acc, w, tokens, boff, lo_off, len, warp, lane);
+      else
+        multiply_stage<D, T, SECOND, NT>(acc, w, tokens, boff, lo_off, len, warp, lane);
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
+      slot.next(ring);
+    }
+    // The warps' sums, in one tree, a group of tokens at a time; half of the warps finish a
+    // group, the others the next.
+    const int row0 = SECOND ? tile * S::kRows : tile * (S::kRows / 2);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j >= nt) break;
+      float4* r = red + buffer * (S::kRed / 16);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        r[(warp * M + m) * 32 + lane] =
+            make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
       consumers_sync();
-      if (half == 0) {
+      const int m = M == 1 ? 0 : warp & 3;
+      if (M == 1 ? warp == item % kConsumers : warp >> 2 == buffer) {
+        float4 v[kConsumers];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j >= nt) break;
-          const float4 o = r[(group * 4 + j) * 32 + lane];
-          const float c[4] = {sum[j][0] + o.x, sum[j][1] + o.y, sum[j][2] + o.z, sum[j][3] + o.w};
-          finish<D, SECOND>(a, tb, u, SECOND ? tile * 64 + group * 16 : tile * 32 + group * 8,
-                            j * 8, lane, c);
-        }
-      }
-    } else {
-      r[warp * 32 + lane] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
-      consumers_sync();
-      // one warp finishes an item, another the next
-      if (warp == (item / (int)gridDim.x) % kConsumers) {
-        float c[2][4];
+        for (int i = 0; i < kConsumers; ++i) v[i] = r[(i * M + m) * 32 + lane];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 v0 = r[(h * 4 + 0) * 32 + lane], v1 = r[(h * 4 + 1) * 32 + lane];
-          const float4 v2 = r[(h * 4 + 2) * 32 + lane], v3 = r[(h * 4 + 3) * 32 + lane];
-          c[h][0] = (v0.x + v1.x) + (v2.x + v3.x);
-          c[h][1] = (v0.y + v1.y) + (v2.y + v3.y);
-          c[h][2] = (v0.z + v1.z) + (v2.z + v3.z);
-          c[h][3] = (v0.w + v1.w) + (v2.w + v3.w);
-        }
-        const float s[4] = {c[0][0] + c[1][0], c[0][1] + c[1][1], c[0][2] + c[1][2],
-                            c[0][3] + c[1][3]};
-        finish<D, SECOND>(a, tb, u, SECOND ? tile * 16 : tile * 8, 0, lane, s);
+        for (int o = 1; o < kConsumers; o *= 2)
+#pragma unroll
+          for (int i = 0; i < kConsumers; i += 2 * o) {
+            v[i].x += v[i + o].x;
+            v[i].y += v[i + o].y;
+            v[i].z += v[i + o].z;
+            v[i].w += v[i + o].w;
+          }
+        const float c[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        finish<D, SECOND>(a, tb, u, row0 + m * (SECOND ? 16 : 8), j * 8, lane, c);
       }
+      buffer ^= 1;      // the next sums must not meet readers of these
     }
-    buffer ^= 1;      // the next item's sums must not meet readers of these
   }
 }
 
@@ -952,7 +937,6 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
 layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMaps maps) {
   using S = Tile<T>;
   __shared__ Tables tb;
-  __shared__ float4 red[2 * kRedBytes / 16];
   __shared__ uint64_t bars[2 * kMaxStages];
   __shared__ int gave_up;
   extern __shared__ __align__(16) uint8_t ring_mem[];
@@ -976,7 +960,8 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   ring.full = bars;
   ring.empty = bars + kMaxStages;
   ring.stage_bytes = (S::kWeightBytes + 2 * tb.most * S::kTokenPitch + 1023) / 1024 * 1024;
-  ring.stages = min(kMaxStages, kRingBytes / ring.stage_bytes);
+  ring.stages = min(kMaxStages, S::kRing / ring.stage_bytes);
+  float4* red = reinterpret_cast<float4*>(ring.base + S::kRing);
   Slot slot(ring);
   if (warp == kConsumers) {
     produce_weights<T, false>(a, maps, tb, ring, slot, g, lane);
@@ -1060,7 +1045,7 @@ int weight_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, i
 
 template <class D, Tiling T>
 int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t stream) {
-  constexpr size_t smem = kRingBytes + 1024;
+  constexpr size_t smem = Tile<T>::kRing + 2 * Tile<T>::kRed + 1024;
   if (int rc = ensure_smem_limit((const void*)layer_experts<D, T>, smem)) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
