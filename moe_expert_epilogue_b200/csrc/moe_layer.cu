@@ -201,7 +201,7 @@ void launch_logits(const Layer& a, cudaStream_t stream) {
 
 // ------------------------------------------------------------ choice
 
-// The logits of token t, experts [lane * V, lane * V + V).
+// The logits of token t (as load_logits).
 template <int V>
 __device__ __forceinline__ void token_logits(const Layer& a, int t, int lane, float (&v)[V]) {
   const int64_t row = (int64_t)t * a.ld_logits;

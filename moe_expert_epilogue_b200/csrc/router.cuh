@@ -24,15 +24,24 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// The logits of experts [lane * V, lane * V + V) of one row; -inf past E.
+// The logits of experts lane, lane + 32, ... of one row; -inf past E.
 template <class D, int V>
 __device__ __forceinline__ void load_logits(const typename D::T* row, int E, int lane,
                                             float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
+    const int e = i * 32 + lane;
     v[i] = e < E ? load1<D>(row + e) : -kInf;
   }
+}
+
+// Sum over all experts of e^{l - top}, experts in the order of load_logits.
+template <int V>
+__device__ __forceinline__ float exp_sum(const float (&v)[V], float top) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) s += v[i] == -kInf ? 0.0f : expf(v[i] - top);
+  return warp_sum(s);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -61,11 +70,31 @@ __device__ __forceinline__ float chosen_score(bool softmax, float v, float top) 
   return 1.0f / (1.0f + expf(-v));
 }
 
-// The K choices of one token from its logits (lane i holds experts i * V ..
-// i * V + V - 1 in v, -inf past the last).  Lane k returns the weight of the
-// k-th choice and its expert in *id (0 and -1 where nothing is left, or k >= K).
-// A choice waits for the one before: the chain of a round is the lanes' maximum,
-// the vote on who holds it, and the removal, without branches.
+// Routing weights of the choices in a warp: `lanes` neighbouring lanes (a power of
+// two) hold a token's, in their order; value -inf and id -1 where there is none.
+// all: softmax over all experts, the sum of e^{l - the token's largest l}.
+__device__ __forceinline__ float choice_weight(float value, int id, int lanes, int lane,
+                                               bool softmax, bool normalise, float scale,
+                                               float all) {
+  const float top = __shfl_sync(kAll, value, lane & ~(lanes - 1));   // the row's largest logit
+  float w = id >= 0 ? chosen_score(softmax, value, top) : 0.0f;
+  if (normalise) {
+    float s = w;
+    for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    w = w / s;
+  } else if (softmax) {
+    w = w / all;
+  } else if (id >= 0) {
+    w = 1.0f / (1.0f + expf(-value));
+  }
+  return id >= 0 ? w * scale : 0.0f;
+}
+
+// The K choices of one token from its logits (as load_logits leaves them).  Lane k
+// returns the weight of the k-th choice and its expert in *id (0 and -1 where
+// nothing is left, or k >= K).  A choice waits for the one before: the chain of a
+// round is the lanes' maximum, the lowest expert that has it, and its removal,
+// without branches.
 template <int V>
 __device__ __forceinline__ float route_token(const float (&v)[V], int K, int lane, bool softmax,
                                              bool normalise, float scale, int* id_out) {
@@ -80,35 +109,19 @@ __device__ __forceinline__ float route_token(const float (&v)[V], int K, int lan
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(kAll, best);
     if (top == 0) break;
-    // the lowest lane, and in it the lowest expert, that holds the largest key
-    const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    bool here = lane == src;
-    int expert = 0;
+    unsigned first = ~0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool hit = here && key[i] == top;
-      key[i] = hit ? 0u : key[i];
-      expert = hit ? lane * V + i : expert;
-      here = here && !hit;
-    }
-    expert = __shfl_sync(kAll, expert, src);
+    for (int i = V - 1; i >= 0; --i) first = key[i] == top ? i * 32 + lane : first;
+    const unsigned expert = __reduce_min_sync(kAll, first);
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = i * 32 + lane == (int)expert ? 0u : key[i];
     mine = lane == k ? key_value(top) : mine;
-    id = lane == k ? expert : id;
+    id = lane == k ? (int)expert : id;
   }
-  const float top = __shfl_sync(kAll, mine, 0);   // the row's largest logit
-  float w = id >= 0 ? chosen_score(softmax, mine, top) : 0.0f;
-  if (softmax && !normalise) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) s += v[i] == -kInf ? 0.0f : expf(v[i] - top);
-    w = w / warp_sum(s);
-  } else if (normalise) {
-    w = w / warp_sum(w);
-  } else if (id >= 0) {
-    w = 1.0f / (1.0f + expf(-mine));
-  }
+  float all = 0.f;
+  if (softmax && !normalise) all = exp_sum<V>(v, __shfl_sync(kAll, mine, 0));
   *id_out = id;
-  return id >= 0 ? w * scale : 0.0f;
+  return choice_weight(mine, id, 32, lane, softmax, normalise, scale, all);
 }
 
 }  // namespace moe

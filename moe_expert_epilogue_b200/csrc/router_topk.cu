@@ -15,8 +15,13 @@
 //                            1 - sig(l_i) for the sigmoid],  0 outside C
 //   sigmoid           dl_i = s g_i sig(l_i) (1 - sig(l_i)),  0 outside C
 //
-// One warp per token; lane i holds the V consecutive experts from i * V (V a
-// power of two, 32 V >= E).
+// One warp per token; lane i holds the experts i, i + 32, ...  The logits are read
+// once and little is written: for many tokens the instructions bound the forward,
+// not HBM.  Each lane sorts its logits once, so that a choice costs one maximum
+// over the lanes and a shift in one of them, and the weights of as many tokens as
+// fit a warp are computed together.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "router.cuh"
@@ -25,23 +30,163 @@ namespace moe {
 
 namespace {
 
+// A logit of a 16-bit type and its expert in one number whose order is the
+// selection's: 0 for -inf, else the upper half as order_key and the lower half
+// falling with the expert, so that no two are equal.
+template <class D>
+__device__ __forceinline__ uint32_t pair_key(uint32_t bits, int e) {
+  constexpr uint32_t kInf16 = std::is_same<D, BF16>::value ? 0x7f80u : 0x7c00u;
+  uint32_t m = bits & 0x8000u ? bits ^ 0xffffu : bits | 0x8000u;
+  m = bits == 0x8000u ? 0x8000u : m;                                   // -0 counts as +0
+  m = (bits & 0x7fffu) > kInf16 ? 0xffffu : m;                         // NaN above everything
+  return bits == (0x8000u | kInf16) ? 0u : m << 16 | (uint32_t)(0xffff - e);
+}
+
+template <class D>
+__device__ __forceinline__ float pair_value(uint32_t key) {
+  const uint32_t m = key >> 16;
+  const uint32_t bits = m & 0x8000u ? m ^ 0x8000u : m ^ 0xffffu;
+  if (std::is_same<D, BF16>::value) return __uint_as_float(bits << 16);
+  return f16_to_f32((uint16_t)bits);
+}
+
+// The sorted logits of a lane: key[] descending, and the experts of fp32 ones.
+template <class D, int V> struct Sorted {                              // 16-bit types
+  uint32_t key[V];
+  __device__ __forceinline__ void set(const uint16_t (&raw)[V], int E, int lane) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 32 + lane;
+      key[i] = e < E ? pair_key<D>(raw[i], e) : 0u;
+    }
+    // Batcher's odd-even merge sort: steps of 2^q within sorted runs of 2^p
+#pragma unroll
+    for (int p = 0; 1 << p < V; ++p)
+#pragma unroll
+      for (int q = p; q >= 0; --q)
+#pragma unroll
+        for (int i = 0; i + (1 << q) < V; ++i) {
+          const int skip = q == p ? 0 : 1 << q;
+          if (i >= skip && (i - skip & (2 << q) - 1) < 1 << q && i >> (p + 1) == i + (1 << q) >> (p + 1)) {
+            const uint32_t lo = min(key[i], key[i + (1 << q)]);
+            key[i] = max(key[i], key[i + (1 << q)]);
+            key[i + (1 << q)] = lo;
+          }
+        }
+  }
+  // Removes the largest left in the warp; false if there is none.
+  __device__ __forceinline__ bool take(float* value, int* expert) {
+    const uint32_t top = __reduce_max_sync(kAll, key[0]);
+    const bool here = key[0] == top;
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = here ? (i + 1 < V ? key[i + 1 < V ? i + 1 : i] : 0u) : key[i];
+    *value = pair_value<D>(top);
+    *expert = 0xffff - (int)(top & 0xffffu);
+    return top != 0;
+  }
+};
+template <int V> struct Sorted<F32, V> {
+  uint32_t key[V];
+  uint32_t at[V];                                                      // experts
+  static constexpr bool kSort = V <= 8;     // beyond, sorting costs more than looking
+  __device__ __forceinline__ void set(const float (&raw)[V], int E, int lane) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      at[i] = i * 32 + lane;
+      key[i] = (int)at[i] < E ? order_key(raw[i]) : 0u;
+    }
+    if (kSort) {
+      // neighbours are exchanged only when out of order: equal ones keep theirs
+#pragma unroll
+      for (int n = 0; n < V; ++n)
+#pragma unroll
+        for (int i = n & 1; i + 1 < V; i += 2) {
+          const bool swap = key[i] < key[i + 1];
+          const uint32_t k0 = key[i], a0 = at[i];
+          key[i] = swap ? key[i + 1] : k0;
+          key[i + 1] = swap ? k0 : key[i + 1];
+          at[i] = swap ? at[i + 1] : a0;
+          at[i + 1] = swap ? a0 : at[i + 1];
+        }
+    }
+  }
+  __device__ __forceinline__ bool take(float* value, int* expert) {
+    uint32_t best = key[0], first = ~0u;
+    if (!kSort) {
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    }
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    if (kSort) {
+      first = key[0] == top ? at[0] : ~0u;
+    } else {
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) first = key[i] == top ? at[i] : first;
+    }
+    const uint32_t e = __reduce_min_sync(kAll, first);
+    const bool here = at[0] == e;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (kSort) {
+        const int n = i + 1 < V ? i + 1 : i;
+        key[i] = here ? (i + 1 < V ? key[n] : 0u) : key[i];
+        at[i] = here && i + 1 < V ? at[n] : at[i];
+      } else {
+        key[i] = at[i] == e ? 0u : key[i];
+      }
+    }
+    *value = key_value(top);
+    *expert = (int)e;
+    return top != 0;
+  }
+};
+
+// `lanes`: K up to a power of two; `group` (a power of two, up to 32 / lanes)
+// neighbouring tokens per warp.
 template <class D, int V>
 __global__ void __launch_bounds__(kThreads)
 router_fwd(const typename D::T* __restrict__ logits, float* __restrict__ weights,
            int32_t* __restrict__ ids, const int32_t* __restrict__ valid, int64_t tokens, int E,
-           int K, int64_t ld, bool softmax, bool normalise, float scale, int32_t* err) {
+           int K, int lanes, int group, int64_t ld, bool softmax, bool normalise, float scale,
+           int32_t* err) {
   pdl_prologue();
   const int lane = threadIdx.x & 31;
   const int64_t n = live_tokens(valid, tokens, err);
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < n; t += step) {
-    float v[V];
-    int id;
-    load_logits<D, V>(logits + t * ld, E, lane, v);
-    const float w = route_token<V>(v, K, lane, softmax, normalise, scale, &id);
-    if (lane < K) {
-      weights[t * K + lane] = w;
-      ids[t * K + lane] = id;
+  const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * group;
+  for (int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * group; t0 < n;
+       t0 += step) {
+    float value = -kInf, all = 0.f;     // lane g * lanes + k: the k-th choice of token t0 + g
+    int id = -1;
+    for (int g = 0; g < group && t0 + g < n; ++g) {
+      const typename D::T* row = logits + (t0 + g) * ld;
+      typename D::T raw[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) raw[i] = i * 32 + lane < E ? __ldg(row + i * 32 + lane) : 0;
+      Sorted<D, V> left;
+      left.set(raw, E, lane);
+      float first = 0.f;
+      for (int k = 0; k < K; ++k) {
+        float v;
+        int e;
+        if (!left.take(&v, &e)) break;
+        if (k == 0) first = v;
+        const bool mine = lane == g * lanes + k;
+        value = mine ? v : value;
+        id = mine ? e : id;
+      }
+      if (softmax && !normalise) {
+        float v[V];
+        load_logits<D, V>(row, E, lane, v);
+        const float s = exp_sum<V>(v, first);
+        all = lane / lanes == g ? s : all;
+      }
+    }
+    const float w = choice_weight(value, id, lanes, lane, softmax, normalise, scale, all);
+    const int64_t t = t0 + lane / lanes;
+    const int k = lane & (lanes - 1);
+    if (k < K && lane / lanes < group && t < n) {
+      weights[t * K + k] = w;
+      ids[t * K + k] = id;
     }
   }
 }
@@ -105,15 +250,12 @@ router_bwd(const typename D::T* __restrict__ logits, const int32_t* __restrict__
     for (int k = 0; k < K; ++k) {
       const int e = __shfl_sync(kAll, id, k);
       const float dk = __shfl_sync(kAll, d, k);
-      if (e >= 0 && e / V == lane) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i == e % V) grad[i] += dk;
-      }
+      for (int i = 0; i < V; ++i) grad[i] += e == i * 32 + lane ? dk : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
+      const int e = i * 32 + lane;
       if (e < E) store1<D>(gl + t * ld_g + e, grad[i]);
     }
   }
@@ -124,11 +266,14 @@ int launch_fwd(const void* logits, float* weights, int32_t* ids, const int32_t* 
                int64_t tokens, int E, int K, int64_t ld, bool softmax, bool normalise,
                float scale, int32_t* err, cudaStream_t stream) {
   auto k = router_fwd<D, V>;
-  int grid = 0;
-  const int64_t per = kThreads / 32;
+  int lanes = 1, grid = 0;
+  while (lanes < K) lanes *= 2;
+  // one token a warp as long as there are warps for them, which is quicker for each token
+  const int group = tokens > 16384 ? 32 / lanes : 1;
+  const int64_t per = (int64_t)(kThreads / 32) * group;
   if (int rc = persistent_grid((const void*)k, 0, (tokens + per - 1) / per, &grid)) return rc;
   launch_kernel(k, grid, 0, stream, static_cast<const typename D::T*>(logits), weights, ids,
-                valid, tokens, E, K, ld, softmax, normalise, scale, err);
+                valid, tokens, E, K, lanes, group, ld, softmax, normalise, scale, err);
   return check_launch();
 }
 
