@@ -12,12 +12,13 @@ namespace moe {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kInf = INFINITY;
 
-// Image of a logit whose unsigned order is the selection's: 0 for -inf (never
-// chosen), all ones for NaN; -0 counts as +0.
+// Image of a logit whose unsigned order is the selection's.  Adding +0 makes -0
+// and +0 one and any NaN the positive one, which then lies above +inf; -inf and
+// what is never a logit (0) do not lie above kDeadKey.
+constexpr uint32_t kDeadKey = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return v == -kInf ? 0u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+  const int32_t b = __float_as_int(__fadd_rn(v, 0.0f));
+  return (uint32_t)(b ^ (b >> 31 | (int32_t)0x80000000));
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) {
@@ -108,7 +109,7 @@ __device__ __forceinline__ float route_token(const float (&v)[V], int K, int lan
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(kAll, best);
-    if (top == 0) break;
+    if (top <= kDeadKey) break;
     unsigned first = ~0u;
 #pragma unroll
     for (int i = V - 1; i >= 0; --i) first = key[i] == top ? i * 32 + lane : first;

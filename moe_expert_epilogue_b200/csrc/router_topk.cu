@@ -31,15 +31,18 @@ namespace moe {
 namespace {
 
 // A logit of a 16-bit type and its expert in one number whose order is the
-// selection's: 0 for -inf, else the upper half as order_key and the lower half
-// falling with the expert, so that no two are equal.
+// selection's: the upper half as order_key, the lower half falling with the
+// expert, so that no two are equal.
 template <class D>
-__device__ __forceinline__ uint32_t pair_key(uint32_t bits, int e) {
-  constexpr uint32_t kInf16 = std::is_same<D, BF16>::value ? 0x7f80u : 0x7c00u;
-  uint32_t m = bits & 0x8000u ? bits ^ 0xffffu : bits | 0x8000u;
-  m = bits == 0x8000u ? 0x8000u : m;                                   // -0 counts as +0
-  m = (bits & 0x7fffu) > kInf16 ? 0xffffu : m;                         // NaN above everything
-  return bits == (0x8000u | kInf16) ? 0u : m << 16 | (uint32_t)(0xffff - e);
+__device__ __forceinline__ uint32_t pair_key(uint16_t raw, uint32_t low) {
+  int32_t b;
+  if (std::is_same<D, BF16>::value) {
+    b = __float_as_int(__fadd_rn(__uint_as_float((uint32_t)raw << 16), 0.0f));
+  } else {
+    asm("add.rn.f16 %0, %0, %1;" : "+h"(raw) : "h"((uint16_t)0));
+    b = (int32_t)((uint32_t)raw << 16);
+  }
+  return ((uint32_t)(b ^ (b >> 31 | (int32_t)0x80000000)) & 0xffff0000u) | low;
 }
 
 template <class D>
@@ -50,14 +53,20 @@ __device__ __forceinline__ float pair_value(uint32_t key) {
   return f16_to_f32((uint16_t)bits);
 }
 
-// The sorted logits of a lane: key[] descending, and the experts of fp32 ones.
+// The logits of a lane, largest first.  take() removes the largest left in the
+// warp and leaves it in `mine` of the lane asked; false if there is none.
+struct Choice {
+  uint32_t key = 0, at = 0;                                            // 0: none
+};
 template <class D, int V> struct Sorted {                              // 16-bit types
   uint32_t key[V];
+  // -inf, as order_key leaves it
+  static constexpr uint32_t kDead = std::is_same<D, BF16>::value ? 0x007fffffu : 0x03ffffffu;
   __device__ __forceinline__ void set(const uint16_t (&raw)[V], int E, int lane) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = i * 32 + lane;
-      key[i] = e < E ? pair_key<D>(raw[i], e) : 0u;
+      key[i] = e < E ? pair_key<D>(raw[i], 0xffffu - e) : 0u;
     }
     // Batcher's odd-even merge sort: steps of 2^q within sorted runs of 2^p
 #pragma unroll
@@ -67,22 +76,28 @@ template <class D, int V> struct Sorted {                              // 16-bit
 #pragma unroll
         for (int i = 0; i + (1 << q) < V; ++i) {
           const int skip = q == p ? 0 : 1 << q;
-          if (i >= skip && (i - skip & (2 << q) - 1) < 1 << q && i >> (p + 1) == i + (1 << q) >> (p + 1)) {
+          if (i >= skip && ((i - skip) & ((2 << q) - 1)) < 1 << q &&
+              i >> (p + 1) == (i + (1 << q)) >> (p + 1)) {
             const uint32_t lo = min(key[i], key[i + (1 << q)]);
             key[i] = max(key[i], key[i + (1 << q)]);
             key[i + (1 << q)] = lo;
           }
         }
   }
-  // Removes the largest left in the warp; false if there is none.
-  __device__ __forceinline__ bool take(float* value, int* expert) {
+  __device__ __forceinline__ bool take(Choice& mine, bool asked) {
     const uint32_t top = __reduce_max_sync(kAll, key[0]);
-    const bool here = key[0] == top;
+    if (top <= kDead) return false;
+    if (key[0] == top) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = here ? (i + 1 < V ? key[i + 1 < V ? i + 1 : i] : 0u) : key[i];
-    *value = pair_value<D>(top);
-    *expert = 0xffff - (int)(top & 0xffffu);
-    return top != 0;
+      for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+      key[V - 1] = 0;
+    }
+    if (asked) mine.key = top;
+    return true;
+  }
+  static __device__ __forceinline__ float value(const Choice& c) { return pair_value<D>(c.key); }
+  static __device__ __forceinline__ int expert(const Choice& c) {
+    return 0xffff - (int)(c.key & 0xffffu);
   }
 };
 template <int V> struct Sorted<F32, V> {
@@ -110,13 +125,14 @@ template <int V> struct Sorted<F32, V> {
         }
     }
   }
-  __device__ __forceinline__ bool take(float* value, int* expert) {
+  __device__ __forceinline__ bool take(Choice& mine, bool asked) {
     uint32_t best = key[0], first = ~0u;
     if (!kSort) {
 #pragma unroll
       for (int i = 1; i < V; ++i) best = max(best, key[i]);
     }
     const uint32_t top = __reduce_max_sync(kAll, best);
+    if (top <= kDeadKey) return false;
     if (kSort) {
       first = key[0] == top ? at[0] : ~0u;
     } else {
@@ -124,21 +140,27 @@ template <int V> struct Sorted<F32, V> {
       for (int i = V - 1; i >= 0; --i) first = key[i] == top ? at[i] : first;
     }
     const uint32_t e = __reduce_min_sync(kAll, first);
-    const bool here = at[0] == e;
+    if (kSort) {
+      if (first == e) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (kSort) {
-        const int n = i + 1 < V ? i + 1 : i;
-        key[i] = here ? (i + 1 < V ? key[n] : 0u) : key[i];
-        at[i] = here && i + 1 < V ? at[n] : at[i];
-      } else {
-        key[i] = at[i] == e ? 0u : key[i];
+        for (int i = 0; i + 1 < V; ++i) {
+          key[i] = key[i + 1];
+          at[i] = at[i + 1];
+        }
+        key[V - 1] = 0;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = at[i] == e ? 0u : key[i];
     }
-    *value = key_value(top);
-    *expert = (int)e;
-    return top != 0;
+    if (asked) {
+      mine.key = top;
+      mine.at = e;
+    }
+    return true;
   }
+  static __device__ __forceinline__ float value(const Choice& c) { return key_value(c.key); }
+  static __device__ __forceinline__ int expert(const Choice& c) { return (int)c.at; }
 };
 
 // `lanes`: K up to a power of two; `group` (a power of two, up to 32 / lanes)
@@ -155,8 +177,8 @@ router_fwd(const typename D::T* __restrict__ logits, float* __restrict__ weights
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * group;
   for (int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * group; t0 < n;
        t0 += step) {
-    float value = -kInf, all = 0.f;     // lane g * lanes + k: the k-th choice of token t0 + g
-    int id = -1;
+    Choice mine;                        // lane g * lanes + k: the k-th choice of token t0 + g
+    float all = 0.f;
     for (int g = 0; g < group && t0 + g < n; ++g) {
       const typename D::T* row = logits + (t0 + g) * ld;
       typename D::T raw[V];
@@ -164,23 +186,18 @@ router_fwd(const typename D::T* __restrict__ logits, float* __restrict__ weights
       for (int i = 0; i < V; ++i) raw[i] = i * 32 + lane < E ? __ldg(row + i * 32 + lane) : 0;
       Sorted<D, V> left;
       left.set(raw, E, lane);
-      float first = 0.f;
-      for (int k = 0; k < K; ++k) {
-        float v;
-        int e;
-        if (!left.take(&v, &e)) break;
-        if (k == 0) first = v;
-        const bool mine = lane == g * lanes + k;
-        value = mine ? v : value;
-        id = mine ? e : id;
-      }
+      for (int k = 0; k < K; ++k)
+        if (!left.take(mine, lane == g * lanes + k)) break;
       if (softmax && !normalise) {
         float v[V];
         load_logits<D, V>(row, E, lane, v);
+        const float first = __shfl_sync(kAll, Sorted<D, V>::value(mine), g * lanes);
         const float s = exp_sum<V>(v, first);
         all = lane / lanes == g ? s : all;
       }
     }
+    const int id = mine.key ? Sorted<D, V>::expert(mine) : -1;
+    const float value = mine.key ? Sorted<D, V>::value(mine) : -kInf;
     const float w = choice_weight(value, id, lanes, lane, softmax, normalise, scale, all);
     const int64_t t = t0 + lane / lanes;
     const int k = lane & (lanes - 1);
@@ -211,10 +228,9 @@ router_bwd(const typename D::T* __restrict__ logits, const int32_t* __restrict__
     const bool live = id >= 0;
     const float l = live ? load1<D>(row + id) : -kInf;
     const float g = live ? __ldg(gw + t * K + lane) * scale : 0.0f;
-    float grad[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) grad[i] = 0.f;
-    float d;
+    typename D::T* out = gl + t * ld_g;
+    float d;                  // gradient of the lane's own choice, beside that of every expert:
+    float rest = 0.0f;
     if (softmax && !normalise) {
       float v[V], top = -kInf, s = 0.f;
       load_logits<D, V>(row, E, lane, v);
@@ -224,15 +240,21 @@ router_bwd(const typename D::T* __restrict__ logits, const int32_t* __restrict__
       if (top == -kInf) top = 0.f;               // every expert closed: all terms are 0
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        if (i * 32 >= E) break;
         v[i] = expf(v[i] - top);
         s += v[i];
       }
       s = warp_sum(s);
-      if (s == 0.0f) s = 1.0f;
-      d = live ? expf(l - top) / s * g : 0.0f;
+      const float inv = s == 0.0f ? 1.0f : 1.0f / s;
+      const float p = live ? expf(l - top) * inv : 0.0f;
+      d = p * g;
       const float dot = warp_sum(d);
 #pragma unroll
-      for (int i = 0; i < V; ++i) grad[i] = -(v[i] / s) * dot;
+      for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        if (e < E) store1<D>(out + e, -(v[i] * inv) * dot);
+      }
+      rest = -p * dot;
     } else {
       const float z = 1.0f / (1.0f + expf(-l));
       if (normalise) {
@@ -245,19 +267,22 @@ router_bwd(const typename D::T* __restrict__ logits, const int32_t* __restrict__
       } else {
         d = live ? g * z * (1.0f / (1.0f + expf(l))) : 0.0f;
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        if (e < E) store1<D>(out + e, 0.0f);
+      }
     }
-    if (!live) d = 0.0f;
+    // The choices' own entries, once the row is written: an expert named twice has both
+    // gradients (each of its lanes stores the same sum).
+    float sum = 0.0f;
     for (int k = 0; k < K; ++k) {
       const int e = __shfl_sync(kAll, id, k);
       const float dk = __shfl_sync(kAll, d, k);
-#pragma unroll
-      for (int i = 0; i < V; ++i) grad[i] += e == i * 32 + lane ? dk : 0.0f;
+      if (e == id) sum += dk;
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
-      if (e < E) store1<D>(gl + t * ld_g + e, grad[i]);
-    }
+    __syncwarp();
+    if (live) store1<D>(out + id, rest + sum);
   }
 }
 
