@@ -20,6 +20,7 @@
 // (16384: forward, in eights) elements take the *_any kernels, which read them
 // again for each pass.
 #include <initializer_list>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -152,10 +153,15 @@ template <class D> struct Unit<D, 8> {
   }
 };
 template <class D> struct Unit<D, 1> {
-  float v0;
-  __device__ __forceinline__ void load(const typename D::T* p) { v0 = load1<D>(p); }
-  __device__ __forceinline__ void load_param(const typename D::T* p) { v0 = load1<D>(p); }
-  __device__ __forceinline__ void widen(float (&v)[1]) const { v[0] = v0; }
+  // (as loaded: widening here would wait for each element before the next is asked for)
+  typename D::T raw;
+  __device__ __forceinline__ void load(const typename D::T* p) { raw = __ldg(p); }
+  __device__ __forceinline__ void load_param(const typename D::T* p) { raw = __ldg(p); }
+  __device__ __forceinline__ void widen(float (&v)[1]) const {
+    if constexpr (std::is_same<D, BF16>::value) v[0] = __uint_as_float((uint32_t)raw << 16);
+    else if constexpr (std::is_same<D, F16>::value) v[0] = f16_to_f32(raw);
+    else v[0] = raw;
+  }
   static __device__ __forceinline__ void store(typename D::T* p, const float (&v)[1]) {
     store1<D>(p, v[0]);
   }
@@ -185,6 +191,18 @@ norm_fwd_rows(const typename D::T* __restrict__ x, const typename W::T* __restri
   };
   auto sum = [&](float v, float* slot) { return TPR == 32 ? warp_sum(v) : cta_sum(v, slot); };
   if (r < rows) load(r);
+  // Single elements: the thread's parameters in registers for all its rows (a load for each
+  // element of each row took as long as the rest).  Eights: from L1 as they are needed.
+  constexpr bool kKeep = VEC == 1;
+  float keep_w[kKeep ? C : 1], keep_b[kKeep ? C : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = c * TPR + t;
+      keep_w[c] = h < hidden ? load1<W>(w + h) : 0.f;
+      keep_b[c] = b && h < hidden ? load1<W>(b + h) : 0.f;
+    }
+  }
   for (; r < rows; r += step) {
     float v[C][VEC];
     float s = 0.f;
@@ -214,17 +232,22 @@ norm_fwd_rows(const typename D::T* __restrict__ x, const typename W::T* __restri
     for (int c = 0; c < C; ++c) {
       const int h = (c * TPR + t) * VEC;
       if (h < hidden) {
-        Unit<W, VEC> u;
-        float p[VEC];
-        u.load_param(w + h);
-        u.widen(p);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[c][i] = v[c][i] * rstd * p[i];
-        if (b) {
-          u.load_param(b + h);
+        if constexpr (kKeep) {
+          v[c][0] = v[c][0] * rstd * keep_w[c];
+          if (b) v[c][0] += keep_b[c];
+        } else {
+          Unit<W, VEC> u;
+          float p[VEC];
+          u.load_param(w + h);
           u.widen(p);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) v[c][i] += p[i];
+          for (int i = 0; i < VEC; ++i) v[c][i] = v[c][i] * rstd * p[i];
+          if (b) {
+            u.load_param(b + h);
+            u.widen(p);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[c][i] += p[i];
+          }
         }
         Unit<D, VEC>::store(y + r * ld_y + h, v[c]);
       }
@@ -644,7 +667,9 @@ int fwd(const void* x_, const void* w_, const void* b_, void* y_, float* mean, f
     return rows_in_registers(norm_fwd_rows<D, W, 8, 8, 256>, 1);
   }
   if (hidden <= 256) return rows_in_registers(norm_fwd_rows<D, W, 1, 8, 32>, 8);
+  if (hidden <= 512) return rows_in_registers(norm_fwd_rows<D, W, 1, 16, 32>, 8);
   if (hidden <= 1024) return rows_in_registers(norm_fwd_rows<D, W, 1, 4, 256>, 1);
+  if (hidden <= 2048) return rows_in_registers(norm_fwd_rows<D, W, 1, 8, 256>, 1);
   if (hidden <= 4096) return rows_in_registers(norm_fwd_rows<D, W, 1, 16, 256>, 1);
   if (hidden <= 8192) return rows_in_registers(norm_fwd_rows<D, W, 1, 32, 256>, 1);
   auto k = norm_fwd_any<D, W>;

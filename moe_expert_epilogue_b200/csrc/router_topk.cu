@@ -68,21 +68,21 @@ template <class D, int V> struct Sorted {                              // 16-bit
       const int e = i * 32 + lane;
       key[i] = e < E ? pair_key<D>(raw[i], 0xffffu - e) : 0u;
     }
-    // Batcher's odd-even merge sort: steps of 2^q within sorted runs of 2^p
+    if constexpr (V > 1) merge<0, 0>();
+  }
+  // Batcher's odd-even merge sort: steps of 2^Q within sorted runs of 2^P.
+  template <int P, int Q> __device__ __forceinline__ void merge() {
+    constexpr int kStep = 1 << Q, kSkip = Q == P ? 0 : kStep;
 #pragma unroll
-    for (int p = 0; 1 << p < V; ++p)
-#pragma unroll
-      for (int q = p; q >= 0; --q)
-#pragma unroll
-        for (int i = 0; i + (1 << q) < V; ++i) {
-          const int skip = q == p ? 0 : 1 << q;
-          if (i >= skip && ((i - skip) & ((2 << q) - 1)) < 1 << q &&
-              i >> (p + 1) == (i + (1 << q)) >> (p + 1)) {
-            const uint32_t lo = min(key[i], key[i + (1 << q)]);
-            key[i] = max(key[i], key[i + (1 << q)]);
-            key[i + (1 << q)] = lo;
-          }
-        }
+    for (int i = kSkip; i + kStep < V; ++i) {
+      if (((i - kSkip) & (2 * kStep - 1)) < kStep && i >> (P + 1) == (i + kStep) >> (P + 1)) {
+        const uint32_t lo = min(key[i], key[i + kStep]);
+        key[i] = max(key[i], key[i + kStep]);
+        key[i + kStep] = lo;
+      }
+    }
+    if constexpr (Q > 0) merge<P, Q - 1>();
+    else if constexpr (2 << P < V) merge<P + 1, P + 1>();
   }
   __device__ __forceinline__ bool take(Choice& mine, bool asked) {
     const uint32_t top = __reduce_max_sync(kAll, key[0]);

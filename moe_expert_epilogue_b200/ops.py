@@ -5,6 +5,7 @@ element of every output is produced by a kernel of libmoe_epilogue.so.
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -375,13 +376,16 @@ def layer_norm_fwd(x, weight, bias=None, eps=1e-5, out=None, mean=None, rstd=Non
     with _place(x.device, stream):
         if out is None:
             out = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+        else:
+            _check(out, "out", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
         if mean is None:
             mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        else:
+            _check(mean, "mean", dtype=torch.float32, numel=rows)
         if rstd is None:
             rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _check(out, "out", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
-        _check(mean, "mean", dtype=torch.float32, numel=rows)
-        _check(rstd, "rstd", dtype=torch.float32, numel=rows)
+        else:
+            _check(rstd, "rstd", dtype=torch.float32, numel=rows)
         ld_x, ld_y = _ld(x, "x"), _ld(out, "out")
         _cuda(x, weight, bias, out, mean, rstd)
         _abi.moe_layer_norm_fwd(x, weight, bias, out, mean, rstd, rows, hidden, ld_x, ld_y, eps,
@@ -403,17 +407,21 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, has_bias=True, grad_x=None, gr
     with _place(x.device, stream):
         if grad_x is None:
             grad_x = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+        else:
+            _check(grad_x, "grad_x", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
         if grad_weight is None:
             grad_weight = torch.empty(hidden, dtype=weight.dtype, device=x.device)
-        if grad_bias is None and has_bias:
+        else:
+            _check(grad_weight, "grad_weight", dtype=weight.dtype, numel=hidden)
+        if grad_bias is not None:
+            _check(grad_bias, "grad_bias", dtype=weight.dtype, numel=hidden)
+        elif has_bias:
             grad_bias = torch.empty(hidden, dtype=weight.dtype, device=x.device)
         if workspace is None:
             workspace = torch.empty(layer_norm_bwd_workspace(rows, hidden), dtype=torch.uint8,
                                     device=x.device)
-        _check(grad_x, "grad_x", dtype=x.dtype, shape=(rows, hidden), contiguous=False)
-        _check(grad_weight, "grad_weight", dtype=weight.dtype, numel=hidden)
-        _check(grad_bias, "grad_bias", dtype=weight.dtype, numel=hidden)
-        _check(workspace, "workspace", dtype=torch.uint8)
+        else:
+            _check(workspace, "workspace", dtype=torch.uint8)
         ld_gy, ld_x, ld_gx = _ld(grad_y, "grad_y"), _ld(x, "x"), _ld(grad_x, "grad_x")
         _cuda(grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias, workspace)
         _abi.moe_layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
@@ -422,6 +430,7 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, has_bias=True, grad_x=None, gr
     return grad_x, grad_weight, grad_bias
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_bwd_workspace(rows, hidden) -> int:
     """Bytes of workspace of layer_norm_bwd."""
     return _abi.moe_layer_norm_bwd_workspace(rows, hidden)
@@ -441,10 +450,12 @@ def router_topk_fwd(logits, top_k, score=MOE_SCORE_SOFTMAX, normalise=True, scal
     with _place(logits.device, stream):
         if weights is None:
             weights = torch.empty(tokens, top_k, dtype=torch.float32, device=logits.device)
+        else:
+            _check(weights, "weights", dtype=torch.float32, shape=(tokens, top_k))
         if ids is None:
             ids = torch.empty(tokens, top_k, dtype=torch.int32, device=logits.device)
-        _check(weights, "weights", dtype=torch.float32, shape=(tokens, top_k))
-        _check(ids, "ids", dtype=torch.int32, shape=(tokens, top_k))
+        else:
+            _check(ids, "ids", dtype=torch.int32, shape=(tokens, top_k))
         ld = _ld(logits, "logits")
         _cuda(logits, weights, ids, valid_tokens, dev_err)
         _abi.moe_router_topk_fwd(logits, moe_dtype(logits.dtype), weights, ids, valid_tokens,
@@ -466,8 +477,9 @@ def router_topk_bwd(logits, ids, grad_weights, score=MOE_SCORE_SOFTMAX, normalis
     with _place(logits.device, stream):
         if grad_logits is None:
             grad_logits = torch.empty(tokens, experts, dtype=logits.dtype, device=logits.device)
-        _check(grad_logits, "grad_logits", dtype=logits.dtype, shape=(tokens, experts),
-               contiguous=False)
+        else:
+            _check(grad_logits, "grad_logits", dtype=logits.dtype, shape=(tokens, experts),
+                   contiguous=False)
         ld, ld_g = _ld(logits, "logits"), _ld(grad_logits, "grad_logits")
         _cuda(logits, ids, grad_weights, grad_logits, valid_tokens, dev_err)
         _abi.moe_router_topk_bwd(logits, moe_dtype(logits.dtype), ids, grad_weights, grad_logits,
@@ -516,11 +528,13 @@ def moe_layer_small_batch(x, w1, w2, top_k, router_weight=None, logits=None,
     with _place(x.device, stream):
         if out is None:
             out = torch.empty(tokens, hidden, dtype=dt, device=x.device)
-        _check(out, "out", dtype=dt, shape=(tokens, hidden), contiguous=False)
+        else:
+            _check(out, "out", dtype=dt, shape=(tokens, hidden), contiguous=False)
         if workspace is None:
             nbytes = moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        _check(workspace, "workspace", dtype=torch.uint8)
+        else:
+            _check(workspace, "workspace", dtype=torch.uint8)
         _cuda(x, w1, w2, router_weight, logits, shared_expert_output, residual, valid_tokens, out,
               topk_weights, topk_ids, workspace, dev_err)
         _abi.moe_layer_small_batch(
@@ -536,6 +550,7 @@ def moe_layer_small_batch(x, w1, w2, top_k, router_weight=None, logits=None,
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k) -> int:
     """Bytes of workspace of moe_layer_small_batch."""
     return _abi.moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k)
