@@ -607,12 +607,43 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, int col
                : "memory");
 }
 
+// The same from the one or two 16-byte words that hold the eight elements, where
+// these lie in [lo, hi): a load for every element took several times as long as
+// the weights' copies.
+__device__ __forceinline__ void copy8_words(uint32_t dst, const uint16_t* row, int col, int len,
+                                            uintptr_t lo, uintptr_t hi) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + col), from = at & ~(uintptr_t)15;
+  const uint32_t shift = (uint32_t)(at - from);
+  if (from < lo || from + 32 > hi) {
+    copy8(dst, row, col, len);
+    return;
+  }
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(from));
+  const uint4 b = __ldg(reinterpret_cast<const uint4*>(from) + 1);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+    const int left = len - col - 2 * i;                       // zeros past the end
+    w[i] = left >= 2 ? w[i] : left == 1 ? w[i] & 0xffffu : 0u;
+  }
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3])
+               : "memory");
+}
+
 // The stages' columns of the unit's tokens (second product: of both halves of
 // their activations), zeros up to a multiple of 8.
 template <Tiling T, bool SECOND>
 __device__ __forceinline__ void produce_tokens(const Layer& a, const Tables& tb, const Ring& ring,
                                                Slot& slot, const GiveUp& g, int warp, int lane) {
   using S = Tile<T>;
+  const auto x_lo = reinterpret_cast<uintptr_t>(a.x);
+  const uintptr_t x_hi = x_lo + (uintptr_t)2 * ((a.tokens - 1) * a.ld_x + a.hidden);
   for_stages<T>(tb, make_product<T, SECOND>(a, tb), [&](Unit u, int, int k0, int len) {
     slot.claim(ring, g);
     const uint32_t dst = tma::smem_addr(ring.base + (size_t)slot.at * ring.stage_bytes) +
@@ -630,7 +661,7 @@ __device__ __forceinline__ void produce_tokens(const Layer& a, const Tables& tb,
       for (int c = lane; c < pieces; c += 32) {
         // (the activation's rows end with zeros up to a multiple of 8)
         if (SECOND || T != kAny) cp_async16(dst + r * S::kTokenPitch + c * 16, src + c * 8);
-        else copy8(dst + r * S::kTokenPitch + c * 16, src, c * 8, len);
+        else copy8_words(dst + r * S::kTokenPitch + c * 16, src, c * 8, len, x_lo, x_hi);
       }
     }
     if (SECOND || T != kAny) cp_async_arrive(&ring.full[slot.at]);
