@@ -29,8 +29,9 @@
 //           (128-byte swizzle)
 //   kNarrow tiles of 16 rows by 1024 columns, up to 8 tokens a unit: one bulk copy
 //           of 2 KB a row
-//   kAny    as kNarrow where rows start off 16-byte boundaries: the copies take
-//           the 16-byte words around a row, and the consumers shift
+//   kAny    as kNarrow (up to 16 tokens) where rows start off 16-byte boundaries:
+//           the copies take the 16-byte words around a weight row, and the
+//           consumers shift; the first kernel lays the tokens out anew
 // Row copies of 512 bytes instead of kWide's boxes were bound by their number:
 // halving their bytes changed nothing.  Four warps to a slice of 128 columns, each
 // with a quarter of the rows, were bound by shared memory in the second product.
@@ -50,9 +51,9 @@ namespace {
 
 constexpr int kMaxTokens = 128, kMaxSlots = 1024, kMaxLayerExperts = 512;
 constexpr int kUnitTokens = 32;                        // tokens of one unit at most,
-constexpr int kNarrowTokens = 8;                       // or in tiles of 16 rows
+constexpr int kNarrowTokens = 8;                       // or in tiles of 16 rows (kAny: 16)
 constexpr int kMaxUnits = kMaxLayerExperts + kMaxSlots / kNarrowTokens;
-constexpr int kBarriers = 2;
+constexpr int kBarriers = 3;      // after the choice, between the products, before the combine
 
 // One expert and up to kUnitTokens (kNarrowTokens) of its tokens.
 struct Unit { uint16_t expert, first, count; };
@@ -91,10 +92,13 @@ struct Layer {
   int32_t* err;
   // workspace
   unsigned* barrier;     // [kBarriers]
+  uint16_t* padded_x;    // kAny: [tokens, hidden up to a multiple of 8], else null
   float* own_logits;     // [tokens, E]
   uint16_t* h;           // [slots, 2, ld_h]: the activation's high and low halves
   int ld_h;              // inter, up to a multiple of 8
   float* y;              // [slots, hidden]
+  float* choice_weight;  // [slots], and
+  int32_t* choice_id;    // of a choice that the CTAs share
 };
 
 // ------------------------------------------------------------ logits
@@ -132,7 +136,16 @@ template <class D, class R, int VEC, int EXPERTS>
 __global__ void __launch_bounds__(kThreads)
 layer_logits(Layer a) {
   pdl_prologue();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kBarriers) a.barrier[threadIdx.x] = 0;
+  const int cta = blockIdx.y * gridDim.x + blockIdx.x, ctas = gridDim.x * gridDim.y;
+  if (cta == 0 && threadIdx.x < kBarriers) a.barrier[threadIdx.x] = 0;
+  if (a.padded_x) {      // the tokens in rows of a multiple of 8 columns, the surplus zero
+    const int ld = (a.hidden + 7) / 8 * 8;
+    for (int i = cta * kThreads + threadIdx.x; i < a.tokens * ld; i += ctas * kThreads) {
+      const int t = i / ld, h = i - t * ld;
+      a.padded_x[i] = h < a.hidden ? __ldg(static_cast<const uint16_t*>(a.x) + t * a.ld_x + h)
+                                   : (uint16_t)0;
+    }
+  }
   if (!a.router_w) return;
   constexpr int N = EXPERTS * kLogitTokens;
   __shared__ double red[kThreads / 32][N];
@@ -193,125 +206,10 @@ void launch_logits(const Layer& a, cudaStream_t stream) {
   const int experts = tiles >= 128 ? 4 : 1;
   const dim3 grid = a.router_w ? dim3((unsigned)((a.E + experts - 1) / experts),
                                       (unsigned)((a.tokens + kLogitTokens - 1) / kLogitTokens))
-                               : dim3(1);
+                               : dim3(a.padded_x ? 64 : 1);
   const auto k = vec ? (experts == 4 ? layer_logits<D, R, 8, 4> : layer_logits<D, R, 8, 1>)
                      : (experts == 4 ? layer_logits<D, R, 1, 4> : layer_logits<D, R, 1, 1>);
   launch_kernel_grid(k, grid, kThreads, 0, stream, a);
-}
-
-// ------------------------------------------------------------ choice
-
-// The logits of token t (as load_logits).
-template <int V>
-__device__ __forceinline__ void token_logits(const Layer& a, int t, int lane, float (&v)[V]) {
-  const int64_t row = (int64_t)t * a.ld_logits;
-  if (a.logits_dt == MOE_FP32)
-    load_logits<F32, V>(static_cast<const float*>(a.logits) + row, a.E, lane, v);
-  else if (a.logits_dt == MOE_BF16)
-    load_logits<BF16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
-  else
-    load_logits<F16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
-}
-
-// The choices of all live tokens, a warp per token, the next one's logits loaded
-// ahead.  (Several tokens side by side took longer: most of a call's time here is
-// the first fetch of the instructions.)
-template <int V>
-__device__ __forceinline__ void choose(const Layer& a, Tables& tb, uint32_t* chosen, int live,
-                                       int threads) {
-  const int warps = threads / 32, lane = threadIdx.x & 31;
-  int t = threadIdx.x >> 5;
-  float next[V];
-  if (t < live) token_logits<V>(a, t, lane, next);
-  for (; t < live; t += warps) {
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = next[i];
-    if (t + warps < live) token_logits<V>(a, t + warps, lane, next);
-    int id;
-    const float w = route_token<V>(v, a.K, lane, a.softmax, a.normalise, a.scale, &id);
-    const unsigned alive = __ballot_sync(kAll, id >= 0);
-    if (lane < a.K) {
-      const int slot = t * a.K + lane;
-      tb.expert[slot] = (int16_t)id;
-      tb.weight[slot] = w;
-      if (id >= 0) atomicOr(&chosen[id * (kMaxTokens / 32) + (t >> 5)], 1u << (t & 31));
-      if (blockIdx.x == 0) {
-        if (a.topk_weights) a.topk_weights[slot] = w;
-        if (a.topk_ids) a.topk_ids[slot] = id;
-      }
-    }
-    if (lane == 0) tb.live[t] = (uint8_t)__popc(alive);
-  }
-}
-
-// Fills the tables, units of at most `unit_tokens`; all `threads` threads of the
-// CTA take part.  chosen [E][kMaxTokens / 32] (scratch): the tokens of each expert
-// as bits, from which counts and places follow without an order of writing.
-__device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int unit_tokens,
-                            int threads) {
-  constexpr int kWords = kMaxTokens / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int live = (int)live_tokens(a.valid, a.tokens, a.err);
-  for (int i = threadIdx.x; i < a.E * kWords; i += threads) chosen[i] = 0;
-  if (threadIdx.x == 0) tb.tokens = live;
-  __syncthreads();
-  if (a.E <= 64) choose<2>(a, tb, chosen, live, threads);
-  else if (a.E <= 256) choose<8>(a, tb, chosen, live, threads);
-  else choose<16>(a, tb, chosen, live, threads);
-  __syncthreads();
-  if (warp == 0) {
-    // the experts' first positions and units
-    int base = 0, units = 0, most = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      int n = 0;
-      if (e < a.E) {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) n += __popc(chosen[e * kWords + i]);
-      }
-      const int u = (n + unit_tokens - 1) / unit_tokens;
-      most = max(most, min(n, unit_tokens));
-      int sum = n | u << 16;                                // inclusive prefix sums
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int before = __shfl_up_sync(kAll, sum, o);
-        if (lane >= o) sum += before;
-      }
-      if (e < a.E) {
-        const int first = base + (sum & 0xffff) - n;
-        tb.first[e] = (uint16_t)first;
-        for (int i = 0; i < u; ++i)
-          tb.unit[units + (sum >> 16) - u + i] = {(uint16_t)e, (uint16_t)(first + i * unit_tokens),
-                                                  (uint16_t)min(unit_tokens, n - i * unit_tokens)};
-      }
-      const int total = __shfl_sync(kAll, sum, 31);
-      base += total & 0xffff;
-      units += total >> 16;
-    }
-    most = __reduce_max_sync(kAll, most);
-    if (lane == 0) {
-      tb.units = units;
-      tb.most = most;
-    }
-  }
-  __syncthreads();
-  for (int s = threadIdx.x; s < live * a.K; s += threads) {
-    const int e = tb.expert[s], t = s / a.K;
-    if (e < 0) continue;
-    int place = 0;             // how many of the token's live experts are lower
-    for (int k = 0; k < a.K; ++k) {
-      const int other = tb.expert[t * a.K + k];
-      place += other >= 0 && other < e;
-    }
-    tb.rank[t * a.K + place] = (uint8_t)(s - t * a.K);
-    int p = tb.first[e] + __popc(chosen[e * kWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
-    for (int i = 0; i < t >> 5; ++i) p += __popc(chosen[e * kWords + i]);
-    tb.position[s] = (uint16_t)p;
-    tb.order[p] = (uint16_t)s;
-    tb.token[p] = (uint8_t)t;
-  }
-  __syncthreads();
 }
 
 // ------------------------------------------------------------ waits
@@ -357,6 +255,166 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
 
+// The load of a value that another CTA wrote before a grid barrier.
+__device__ __forceinline__ float ld_cg(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ int32_t ld_cg(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------ choice
+
+// The logits of token t (as load_logits).
+template <int V>
+__device__ __forceinline__ void token_logits(const Layer& a, int t, int lane, float (&v)[V]) {
+  const int64_t row = (int64_t)t * a.ld_logits;
+  if (a.logits_dt == MOE_FP32)
+    load_logits<F32, V>(static_cast<const float*>(a.logits) + row, a.E, lane, v);
+  else if (a.logits_dt == MOE_BF16)
+    load_logits<BF16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
+  else
+    load_logits<F16, V>(static_cast<const uint16_t*>(a.logits) + row, a.E, lane, v);
+}
+
+// The choices of the tokens t, t + step, ... below `live` by one warp, the next
+// one's logits loaded ahead; take(slot, expert, weight) in lane k for the k-th.
+// (Several tokens side by side took longer: much of the time here is the first
+// fetch of the instructions.)
+template <int V, class F>
+__device__ __forceinline__ void choose(const Layer& a, int t, int step, int live, F take) {
+  const int lane = threadIdx.x & 31;
+  float next[V];
+  if (t < live) token_logits<V>(a, t, lane, next);
+  for (; t < live; t += step) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = next[i];
+    if (t + step < live) token_logits<V>(a, t + step, lane, next);
+    int id;
+    const float w = route_token<V>(v, a.K, lane, a.softmax, a.normalise, a.scale, &id);
+    if (lane < a.K) take(t * a.K + lane, id, w);
+  }
+}
+
+template <class F>
+__device__ __forceinline__ void choose(const Layer& a, int t, int step, int live, F take) {
+  if (a.E <= 64) choose<2>(a, t, step, live, take);
+  else if (a.E <= 256) choose<8>(a, t, step, live, take);
+  else choose<16>(a, t, step, live, take);
+}
+
+// Fills the tables, units of at most `unit_tokens`; all `threads` threads of the
+// CTA take part.  chosen [E][kMaxTokens / 32] (scratch): the tokens of each expert
+// as bits, from which counts and places follow without an order of writing.
+//   A choice takes a warp about 2 us.  Up to two tokens a warp every CTA makes
+// them all; more are shared among the CTAs, at the price of a grid barrier (64
+// tokens of 64 experts: 12 us down to 5).
+__device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int unit_tokens,
+                            int threads, const GiveUp& g) {
+  constexpr int kWords = kMaxTokens / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = threads / 32;
+  const int live = (int)live_tokens(a.valid, a.tokens, a.err);
+  for (int i = threadIdx.x; i < a.E * kWords; i += threads) chosen[i] = 0;
+  if (threadIdx.x == 0) tb.tokens = live;
+  __syncthreads();
+  const auto enter = [&](int slot, int id, float w) {
+    const int t = slot / a.K;
+    tb.expert[slot] = (int16_t)id;
+    tb.weight[slot] = w;
+    if (id >= 0) atomicOr(&chosen[id * kWords + (t >> 5)], 1u << (t & 31));
+  };
+  const auto report = [&](int slot, int id, float w) {
+    if (a.topk_weights) a.topk_weights[slot] = w;
+    if (a.topk_ids) a.topk_ids[slot] = id;
+  };
+  if (live <= 2 * warps) {
+    choose(a, warp, warps, live, [&](int slot, int id, float w) {
+      enter(slot, id, w);
+      if (blockIdx.x == 0) report(slot, id, w);
+    });
+  } else {
+    if (warp == 0) {
+      choose(a, blockIdx.x, gridDim.x, live, [&](int slot, int id, float w) {
+        a.choice_weight[slot] = w;
+        a.choice_id[slot] = id;
+        report(slot, id, w);
+      });
+      __syncwarp();
+      if (lane == 0) {
+        grid_arrive(&a.barrier[0]);
+        grid_wait(&a.barrier[0], g);
+      }
+    }
+    __syncthreads();
+    const bool none = *g.flag;           // after a wait that gave up they may be anything
+    for (int s = threadIdx.x; s < live * a.K; s += threads)
+      enter(s, none ? -1 : ld_cg(a.choice_id + s), ld_cg(a.choice_weight + s));
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // the experts' first positions and units
+    int base = 0, units = 0, most = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      int n = 0;
+      if (e < a.E) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) n += __popc(chosen[e * kWords + i]);
+      }
+      const int u = (n + unit_tokens - 1) / unit_tokens;
+      most = max(most, min(n, unit_tokens));
+      int sum = n | u << 16;                                // inclusive prefix sums
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int before = __shfl_up_sync(kAll, sum, o);
+        if (lane >= o) sum += before;
+      }
+      if (e < a.E) {
+        const int first = base + (sum & 0xffff) - n;
+        tb.first[e] = (uint16_t)first;
+        for (int i = 0; i < u; ++i)
+          tb.unit[units + (sum >> 16) - u + i] = {(uint16_t)e, (uint16_t)(first + i * unit_tokens),
+                                                  (uint16_t)min(unit_tokens, n - i * unit_tokens)};
+      }
+      const int total = __shfl_sync(kAll, sum, 31);
+      base += total & 0xffff;
+      units += total >> 16;
+    }
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 0) {
+      tb.units = units;
+      tb.most = most;
+    }
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < live; t += threads) {
+    int n = 0;
+    for (int k = 0; k < a.K; ++k) n += tb.expert[t * a.K + k] >= 0;
+    tb.live[t] = (uint8_t)n;
+  }
+  for (int s = threadIdx.x; s < live * a.K; s += threads) {
+    const int e = tb.expert[s], t = s / a.K;
+    if (e < 0) continue;
+    int place = 0;             // how many of the token's live experts are lower
+    for (int k = 0; k < a.K; ++k) {
+      const int other = tb.expert[t * a.K + k];
+      place += other >= 0 && other < e;
+    }
+    tb.rank[t * a.K + place] = (uint8_t)(s - t * a.K);
+    int p = tb.first[e] + __popc(chosen[e * kWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
+    for (int i = 0; i < t >> 5; ++i) p += __popc(chosen[e * kWords + i]);
+    tb.position[s] = (uint16_t)p;
+    tb.order[p] = (uint16_t)s;
+    tb.token[p] = (uint8_t)t;
+  }
+  __syncthreads();
+}
+
 // ------------------------------------------------------------ products
 
 __device__ __forceinline__ float activation(float g, float u, float p, float L) {
@@ -374,13 +432,6 @@ __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
   const float h = round_to<D>(inf ? v : clamp_sym(v, kMax));
   store1<D>(hi, h);
   store1<D>(lo, inf ? 0.0f : v - h);
-}
-
-// The load of a value that another CTA wrote before a grid barrier.
-__device__ __forceinline__ float ld_cg(const float* p) {
-  float v;
-  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
 }
 
 __device__ __forceinline__ void ld_cg4(const float* p, float* v) {
@@ -407,7 +458,8 @@ struct Tile {
   static constexpr int kTokenPitch = kCols * 2 + 16;
   static constexpr int kPitch = T == kAny ? kCols * 2 + 32 : kCols * 2 + 16;   // not of kWide
   static constexpr int kWeightBytes = T == kWide ? kRows * kCols * 2 : kRows * kPitch;
-  static constexpr int kTokens = T == kWide ? kUnitTokens : kNarrowTokens;
+  static constexpr int kTokens = T == kWide ? kUnitTokens : T == kAny ? 2 * kNarrowTokens
+                                                                      : kNarrowTokens;
   // one buffer of the warps' sums; the ring: stages of weights, then up to 2 * most token rows
   static constexpr int kRed = kConsumers * (kRows / 16) * 32 * 16;
   static constexpr int kRing = (232448 - (int)sizeof(Tables) - 512 - 2 * kRed - 1024) / 1024 * 1024;
@@ -416,7 +468,7 @@ struct Tile {
 static_assert(Tile<kWide>::kRing >= 2 * (Tile<kWide>::kWeightBytes +
                                          2 * kUnitTokens * Tile<kWide>::kTokenPitch + 1023) &&
                   Tile<kAny>::kRing >= 2 * (Tile<kAny>::kWeightBytes +
-                                            2 * kNarrowTokens * Tile<kAny>::kTokenPitch + 1023),
+                                            4 * kNarrowTokens * Tile<kAny>::kTokenPitch + 1023),
               "two stages at least");
 static_assert(Tile<kWide>::kRing >= kMaxLayerExperts * (kMaxTokens / 32) * 4,
               "room for make_tables' scratch");
@@ -591,59 +643,12 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Columns [col, col + 8) of a row of `len` columns into shared memory, zeros
-// past the end, element by element.
-__device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, int col, int len) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = col + 2 * i;
-    const uint32_t lo = c < len ? __ldg(row + c) : 0u;
-    const uint32_t hi = c + 1 < len ? __ldg(row + c + 1) : 0u;
-    w[i] = lo | hi << 16;
-  }
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3])
-               : "memory");
-}
-
-// The same from the one or two 16-byte words that hold the eight elements, where
-// these lie in [lo, hi): a load for every element took several times as long as
-// the weights' copies.
-__device__ __forceinline__ void copy8_words(uint32_t dst, const uint16_t* row, int col, int len,
-                                            uintptr_t lo, uintptr_t hi) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + col), from = at & ~(uintptr_t)15;
-  const uint32_t shift = (uint32_t)(at - from);
-  if (from < lo || from + 32 > hi) {
-    copy8(dst, row, col, len);
-    return;
-  }
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(from));
-  const uint4 b = __ldg(reinterpret_cast<const uint4*>(from) + 1);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
-    const int left = len - col - 2 * i;                       // zeros past the end
-    w[i] = left >= 2 ? w[i] : left == 1 ? w[i] & 0xffffu : 0u;
-  }
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3])
-               : "memory");
-}
-
 // The stages' columns of the unit's tokens (second product: of both halves of
-// their activations), zeros up to a multiple of 8.
+// their activations).  Both lie in rows that end with zeros up to a multiple of 8.
 template <Tiling T, bool SECOND>
 __device__ __forceinline__ void produce_tokens(const Layer& a, const Tables& tb, const Ring& ring,
                                                Slot& slot, const GiveUp& g, int warp, int lane) {
   using S = Tile<T>;
-  const auto x_lo = reinterpret_cast<uintptr_t>(a.x);
-  const uintptr_t x_hi = x_lo + (uintptr_t)2 * ((a.tokens - 1) * a.ld_x + a.hidden);
   for_stages<T>(tb, make_product<T, SECOND>(a, tb), [&](Unit u, int, int k0, int len) {
     slot.claim(ring, g);
     const uint32_t dst = tma::smem_addr(ring.base + (size_t)slot.at * ring.stage_bytes) +
@@ -658,14 +663,10 @@ __device__ __forceinline__ void produce_tokens(const Layer& a, const Tables& tb,
         src = static_cast<const uint16_t*>(a.x) + tb.token[u.first + r] * a.ld_x + k0;
       }
 #pragma unroll 4
-      for (int c = lane; c < pieces; c += 32) {
-        // (the activation's rows end with zeros up to a multiple of 8)
-        if (SECOND || T != kAny) cp_async16(dst + r * S::kTokenPitch + c * 16, src + c * 8);
-        else copy8_words(dst + r * S::kTokenPitch + c * 16, src, c * 8, len, x_lo, x_hi);
-      }
+      for (int c = lane; c < pieces; c += 32)
+        cp_async16(dst + r * S::kTokenPitch + c * 16, src + c * 8);
     }
-    if (SECOND || T != kAny) cp_async_arrive(&ring.full[slot.at]);
-    else tma::mbar_arrive(&ring.full[slot.at]);
+    cp_async_arrive(&ring.full[slot.at]);
     slot.next(ring);
   });
 }
@@ -868,11 +869,12 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
         w[m].row8 = rel[m].row8 + stage;
       }
       const uint32_t tokens = stage + S::kWeightBytes + (lane >> 3) * 16;
-      // (a third group of tokens goes with a fourth, which repeats the last token)
       if (NT == 1 || nt == 1)
         multiply_stage<D, T, SECOND, 1>(acc, w, tokens, boff, lo_off, len, warp, lane);
       else if (nt == 2)
         multiply_stage<D, T, SECOND, NT < 2 ? 1 : 2>(acc, w, tokens, boff, lo_off, len, warp, lane);
+      else if (nt == 3)
+        multiply_stage<D, T, SECOND, NT < 3 ? 1 : 3>(acc, w, tokens, boff, lo_off, len, warp, lane);
       else
         multiply_stage<D, T, SECOND, NT>(acc, w, tokens, boff, lo_off, len, warp, lane);
       __syncwarp();
@@ -982,10 +984,10 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   }
   pdl_prologue();
   // (the ring serves as scratch before its first copies)
-  make_tables(a, tb, reinterpret_cast<uint32_t*>(ring_mem), S::kTokens, kLayerThreads);
+  const GiveUp g{&gave_up, a.err};
+  make_tables(a, tb, reinterpret_cast<uint32_t*>(ring_mem), S::kTokens, kLayerThreads, g);
   fence_async_proxy();                   // ... by bulk copies
   __syncthreads();
-  const GiveUp g{&gave_up, a.err};
   Ring ring;
   ring.base = ring_mem + ((1024u - (tma::smem_addr(ring_mem) & 1023u)) & 1023u);
   ring.full = bars;
@@ -1003,7 +1005,7 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   if (warp > kConsumers) {
     const int w = warp - kConsumers - 1;
     produce_tokens<T, false>(a, tb, ring, slot, g, w, lane);
-    if (lane == 0) grid_wait(&a.barrier[0], g);
+    if (lane == 0) grid_wait(&a.barrier[1], g);
     __syncwarp();
     produce_tokens<T, true>(a, tb, ring, slot, g, w, lane);
     cp_async_wait();
@@ -1012,12 +1014,12 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   int buffer = 0;
   consume<D, T, false>(a, tb, ring, slot, red, buffer, g);
   consumers_sync();
-  if (threadIdx.x == 0) grid_arrive(&a.barrier[0]);
+  if (threadIdx.x == 0) grid_arrive(&a.barrier[1]);
   consume<D, T, true>(a, tb, ring, slot, red, buffer, g);
   consumers_sync();
   if (threadIdx.x == 0) {
-    grid_arrive(&a.barrier[1]);
-    grid_wait(&a.barrier[1], g);
+    grid_arrive(&a.barrier[2]);
+    grid_wait(&a.barrier[2], g);
   }
   consumers_sync();
   if (a.eights) combine<D, 8>(a, tb);
@@ -1029,12 +1031,15 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
 inline int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Byte offsets of the workspace's parts, and its size.
-struct Space { int64_t logits, h, y, bytes; };
+struct Space { int64_t logits, weight, id, x, h, y, bytes; };
 
 Space layer_space(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K) {
   Space s;
   s.logits = 256;                                        // the barrier words come first
-  s.h = s.logits + up256(tokens * E * 4);
+  s.weight = s.logits + up256(tokens * E * 4);
+  s.id = s.weight + up256(tokens * K * 4);
+  s.x = s.id + up256(tokens * K * 4);
+  s.h = s.x + up256(tokens * ((hidden + 7) / 8 * 8) * 2);
   s.y = s.h + up256(tokens * K * 2 * ((inter + 7) / 8 * 8) * 2);
   s.bytes = s.y + up256(tokens * K * hidden * 4);
   return s;
@@ -1094,21 +1099,37 @@ int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t
   return check_launch();
 }
 
+// Time (us) of both products in tiles of `rows` rows: the rounds of items over the
+// SMs, an item by the bytes that an SM's share of HBM brings (44 KB a us), but at
+// least the 0.75 us that a CTA needs from one item to the next.
+double tiles_time(const Layer& a, int rows, int sms) {
+  const int64_t experts = a.E < (int64_t)a.tokens * a.K ? a.E : a.tokens * a.K;
+  const auto product = [&](int64_t row_count, int64_t axis) {
+    const int64_t items = experts * ((row_count + rows - 1) / rows);
+    const double one = (double)rows * axis * 2 / 44e3;
+    return (double)((items + sms - 1) / sms) * (one > 0.75 ? one : 0.75);
+  };
+  return product(2 * (int64_t)a.inter, a.hidden) + product(a.hidden, a.inter);
+}
+
 template <class D>
-int launch(const Layer& a, cudaStream_t stream) {
-  if (a.router_f32) launch_logits<D, F32>(a, stream);
-  else launch_logits<D, D>(a, stream);
+int launch(const Layer& given, cudaStream_t stream) {
+  if (given.router_f32) launch_logits<D, F32>(given, stream);
+  else launch_logits<D, D>(given, stream);
   if (int rc = check_launch()) return rc;
   int sms = 0;
   if (int rc = device_sm_count(&sms)) return rc;
   WeightMaps maps = {};
-  if (a.hidden % 8 != 0 || a.ld_x % 8 != 0 || a.inter % 8 != 0 || !aligned16(a.x) ||
-      !aligned16(a.w1) || !aligned16(a.w2))
+  Layer a = given;
+  if (a.padded_x) {
+    a.x = a.padded_x;
+    a.ld_x = (a.hidden + 7) / 8 * 8;
     return launch_experts<D, kAny>(a, maps, sms, stream);
-  // tiles of 16 rows for a few tokens whose experts make few tiles of 64: with fewer than 8 of
-  // these a CTA, the last round would leave up to an eighth of the time of some CTAs idle
-  const int64_t experts = a.E < (int64_t)a.tokens * a.K ? a.E : a.tokens * a.K;
-  if ((a.tokens <= kNarrowTokens && experts * ((a.inter + 31) / 32) < 8 * (int64_t)sms) ||
+  }
+  // The narrow tiles' units hold 8 tokens: more tokens may need the weights again.  One token
+  // of eight 4096 x 2048 experts: 75 us in narrow tiles, 86 in wide ones; eight tokens of 64
+  // experts of 2048 x 512: 78 and 63.
+  if ((a.tokens <= kNarrowTokens && tiles_time(a, 16, sms) <= tiles_time(a, 64, sms)) ||
       a.inter == 0)
     return launch_experts<D, kNarrow>(a, maps, sms, stream);
   if (int rc = weight_map(&maps.w1, a.w1, a.hidden, a.inter, 2 * (int64_t)a.E, 32)) return rc;
@@ -1144,7 +1165,12 @@ int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream) {
   a.own_logits = reinterpret_cast<float*>(ws + s.logits);
   a.h = reinterpret_cast<uint16_t*>(ws + s.h);
   a.y = reinterpret_cast<float*>(ws + s.y);
+  a.choice_weight = reinterpret_cast<float*>(ws + s.weight);
+  a.choice_id = reinterpret_cast<int32_t*>(ws + s.id);
   a.ld_h = (m.inter + 7) / 8 * 8;
+  if (m.hidden % 8 != 0 || m.ld_x % 8 != 0 || m.inter % 8 != 0 || !aligned16(m.x) ||
+      !aligned16(m.w1) || !aligned16(m.w2))
+    a.padded_x = reinterpret_cast<uint16_t*>(ws + s.x);
   a.eights = m.hidden % kVec == 0 && m.ld_out % kVec == 0 && aligned16(m.out) &&
              (!m.shared || (m.ld_shared % kVec == 0 && aligned16(m.shared))) &&
              (!m.residual || (m.ld_residual % kVec == 0 && aligned16(m.residual)));
