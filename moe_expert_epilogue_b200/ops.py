@@ -43,11 +43,11 @@ def _check(t, name, dtype=None, shape=None, numel=None, contiguous=True):
     trusts the sizes it is given, so a mismatch must stop here."""
     if t is None:
         return
-    if dtype is not None:
+    if dtype is not None and t.dtype is not dtype:
         allowed = dtype if isinstance(dtype, tuple) else (dtype,)
         if t.dtype not in allowed:
             raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, allowed))}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
@@ -353,6 +353,8 @@ _HERE = contextlib.nullcontext()
 
 def _ld(t, name):
     """Leading dimension; of a single row whatever its stride says."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t.shape[1]
     return max(_rows_stride(t, name), t.shape[1])
 
 
