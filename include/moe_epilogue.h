@@ -30,11 +30,11 @@
  *     vectorised path (for 16-bit data, 32-byte aligned pointers and widths
  *     that are multiples of 16 take 32-byte accesses where that is faster);
  *     anything else takes an element-wise path inside the same kernel family
- *     with identical results (grad_probs, a reduction: within its stated
- *     tolerance, its order fixed for a given layout).
+ *     with identical results (grad_probs and the layer norm's sums: within
+ *     their tolerance, the order fixed for a given layout).
  *   - Aliasing: outputs must not overlap inputs, except that
- *     moe_residual_add and moe_epilogue_fused may run in place
- *     (out == residual).
+ *     moe_residual_add, moe_epilogue_fused and moe_layer_small_batch may run
+ *     in place (out == residual).
  *   - Errors: the return value is MOE_OK or one of the MOE_ERR_* codes below.
  *     Argument errors are detected before anything is enqueued.  MOE_ERR_CUDA
  *     means a CUDA runtime call failed (moe_last_cuda_error() gives the
@@ -466,9 +466,9 @@ MOE_API int moe_layer_norm_fwd(const void* x, const void* weight, const void* bi
  *   grad_x[r, h]   = rstd * (a - 1/hidden sum_h a - xhat * 1/hidden sum_h a * xhat)
  *   grad_weight[h] = sum_r grad_y * xhat,   grad_bias[h] = sum_r grad_y
  * fp32 sums, one rounding to dt / w_dt.  The sums over the rows run in a fixed
- * order that depends on rows, hidden and the alignment of the data alone; over
- * no rows they are +0.  Enqueues two kernels (three for rows of more than 8192
- * columns): the rows, then the partial sums of the row groups.
+ * order that depends on rows, hidden, the types and the alignment of the data
+ * alone; over no rows they are +0.  Enqueues two kernels (three for rows of more
+ * than 8192 columns): the rows, then the partial sums of the row groups.
  * mean, rstd   fp32 [rows], from the forward
  * grad_bias    w_dt [hidden] or NULL (no bias)
  * workspace    at least moe_layer_norm_bwd_workspace() bytes, 16-byte aligned

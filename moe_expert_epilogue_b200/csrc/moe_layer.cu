@@ -454,9 +454,10 @@ template <Tiling T>
 struct Tile {
   static constexpr int kRows = T == kWide ? 64 : 16;
   static constexpr int kCols = T == kWide ? kSplitCols : 4 * kSplitCols;
-  // rows of an odd multiple of 16 bytes: ldmatrix without bank conflicts
+  // Rows of an odd multiple of 16 bytes: ldmatrix without bank conflicts.  A row of kAny
+  // fills its pitch; what is read past its end is not used.
   static constexpr int kTokenPitch = kCols * 2 + 16;
-  static constexpr int kPitch = T == kAny ? kCols * 2 + 32 : kCols * 2 + 16;   // not of kWide
+  static constexpr int kPitch = kCols * 2 + 16;                    // not of kWide
   static constexpr int kWeightBytes = T == kWide ? kRows * kCols * 2 : kRows * kPitch;
   static constexpr int kTokens = T == kWide ? kUnitTokens : T == kAny ? 2 * kNarrowTokens
                                                                       : kNarrowTokens;
