@@ -129,8 +129,8 @@ MOE_API int moe_abi_version(void);
 
 /* Error bits recorded on the current device by calls that were given no
  * error word of their own (today: the TMA-staged clamped-SwiGLU forward
- * through moe_swiglu_clamped_fwd, or _ex with dev_err NULL, and the layer
- * norm's backward: MOE_DEVERR_TIMEOUT).  One word per device, shared by every stream and
+ * through moe_swiglu_clamped_fwd, or _ex with dev_err NULL, the layer norm's
+ * backward, and moe_layer_small_batch with dev_err NULL: MOE_DEVERR_TIMEOUT).  One word per device, shared by every stream and
  * thread; pass dev_err to moe_swiglu_clamped_fwd_ex to keep a call's bits
  * apart.  Synchronous: waits for the device, copies the word into *bits and,
  * if `clear`, resets it.  Returns MOE_OK, MOE_ERR_NULL or MOE_ERR_CUDA. */
@@ -564,7 +564,8 @@ MOE_API int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t*
  * limit           as moe_swiglu_clamped_fwd;  score, normalise, scale as
  *                 moe_router_topk_fwd
  * dev_err         optional int32 (device): MOE_DEVERR_COUNT; MOE_DEVERR_TIMEOUT
- *                 if a wait gave up (~1 s)
+ *                 if a wait gave up (~1 s; without dev_err in the word of
+ *                 moe_device_errors): the results are void
  * ---------------------------------------------------------------------- */
 MOE_API int moe_layer_small_batch_workspace(int64_t tokens, int64_t hidden, int64_t inter,
                                             int32_t num_experts, int32_t top_k, int64_t* bytes);

@@ -157,6 +157,8 @@ struct MoeLayerArgs {
   float scale, limit;
   int32_t* err;
 };
+// Copies (and optionally clears) the few-token layer's per-device timeout word.
+int moe_layer_device_errors(int32_t* bits, int clear);
 bool moe_layer_shape_ok(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K);
 int64_t moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K);
 int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream);

@@ -55,6 +55,10 @@ constexpr int kNarrowTokens = 8;                       // or in tiles of 16 rows
 constexpr int kMaxUnits = kMaxLayerExperts + kMaxSlots / kNarrowTokens;
 constexpr int kBarriers = 3;      // after the choice, between the products, before the combine
 
+// Error bits of waits that gave up in calls without an error word of their own
+// (read by moe_device_errors).
+__device__ int32_t g_layer_errors;
+
 // One expert and up to kUnitTokens (kNarrowTokens) of its tokens.
 struct Unit { uint16_t expert, first, count; };
 
@@ -985,7 +989,7 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   }
   pdl_prologue();
   // (the ring serves as scratch before its first copies)
-  const GiveUp g{&gave_up, a.err};
+  const GiveUp g{&gave_up, a.err ? a.err : &g_layer_errors};
   make_tables(a, tb, reinterpret_cast<uint32_t*>(ring_mem), S::kTokens, kLayerThreads, g);
   fence_async_proxy();                   // ... by bulk copies
   __syncthreads();
@@ -1144,6 +1148,17 @@ bool moe_layer_shape_ok(int64_t tokens, int64_t hidden, int64_t inter, int64_t E
   return tokens >= 0 && tokens <= kMaxTokens && E >= 1 && E <= kMaxLayerExperts && K >= 1 &&
          K <= 32 && K <= E && tokens * K <= kMaxSlots && hidden >= 0 && inter >= 0 &&
          hidden <= (1 << 20) && inter <= (1 << 20);
+}
+
+int moe_layer_device_errors(int32_t* bits, int clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_layer_errors, sizeof(int32_t));
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (clear) {
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_layer_errors, &zero, sizeof(int32_t));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return MOE_OK;
 }
 
 int64_t moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K) {

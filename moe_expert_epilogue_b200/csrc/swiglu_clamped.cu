@@ -663,5 +663,8 @@ extern "C" int moe_device_errors(int32_t* bits, int clear) {
   int32_t norm = 0;
   if (int rc = moe::layer_norm_device_errors(&norm, clear)) return rc;
   *bits |= norm;
+  int32_t layer = 0;
+  if (int rc = moe::moe_layer_device_errors(&layer, clear)) return rc;
+  *bits |= layer;
   return MOE_OK;
 }

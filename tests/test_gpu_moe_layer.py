@@ -367,3 +367,63 @@ def test_the_block_of_a_decode_step(cuda_device):
     # that path rounds to bf16 at the products, the activation, each row, the sum and the output
     scale = want.abs() + d["shared_expert_output"].double().abs() + d["residual"].double().abs() + 2
     assert ((a.double() - many.double()).abs() <= 8 * 2.0 ** -8 * scale).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 30])
+def test_captured_before_any_eager_call_of_its_shape(cuda_device, tokens):
+    """A graph whose capture is the first call of these sizes; two replays of it in flight on
+    one stream behind changing inputs."""
+    d = _inputs(tokens, 712, 88, 24, bf, cuda_device, seed=31)
+    ws = torch.empty(ops.moe_layer_small_batch_workspace(tokens, 712, 88, 24, 5),
+                     dtype=torch.uint8, device=cuda_device)
+    out = torch.zeros(tokens, 712, dtype=bf, device=cuda_device)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.moe_layer_small_batch(d["x"], d["w1"], d["w2"], 5, router_weight=d["router_weight"],
+                                  residual=d["residual"], out=out, workspace=ws)
+    x0 = d["x"].clone()
+    g.replay()
+    first = out.clone()
+    d["x"].neg_()
+    g.replay()
+    second = out.clone()
+    d["x"].copy_(x0)
+    kw = dict(router_weight=d["router_weight"], residual=d["residual"])
+    assert torch.equal(first, ops.moe_layer_small_batch(x0, d["w1"], d["w2"], 5, **kw))
+    assert torch.equal(second, ops.moe_layer_small_batch(-x0, d["w1"], d["w2"], 5, **kw))
+
+
+@pytest.mark.parametrize("fill", ["nan", "inf"])
+def test_a_bad_token_stays_with_itself(cuda_device, fill):
+    """A token whose input is not finite spoils its own row alone."""
+    d = _inputs(20, 520, 136, 9, bf, cuda_device, seed=33)
+    logits = torch.randn(20, 9, device=cuda_device,
+                         generator=torch.Generator(device=cuda_device).manual_seed(34))
+    want, _, _ = _run(d, 3, logits=logits)
+    d["x"][7] = float(fill)
+    got, _, _ = _run(d, 3, logits=logits)
+    keep = [t for t in range(20) if t != 7]
+    assert torch.equal(got[keep], want[keep]) and not got[7].isfinite().any()
+
+
+def test_weights_past_32_bits(cuda_device):
+    """Experts whose weights start beyond 2^31 elements."""
+    e, inter, hid = 400, 2048, 2112
+    d = _inputs(2, hid, 8, 1, bf, cuda_device, seed=35)
+    w1 = torch.empty(e, 2 * inter, hid, dtype=bf, device=cuda_device)
+    w2 = torch.empty(e, hid, inter, dtype=bf, device=cuda_device)
+    assert w1.numel() > 2 ** 31 and w1.numel() + w2.numel() > 2 ** 32
+    g = torch.Generator(device=cuda_device).manual_seed(36)
+    for i in (0, e - 1):
+        w1[i] = (torch.randn(2 * inter, hid, generator=g, device=cuda_device) * hid ** -0.5).to(bf)
+        w2[i] = (torch.randn(hid, inter, generator=g, device=cuda_device) * inter ** -0.5).to(bf)
+    logits = torch.full((2, e), -INF, device=cuda_device)
+    logits[0, e - 1] = 1.0
+    logits[1, 0], logits[1, e - 1] = 0.5, 0.25
+    out = ops.moe_layer_small_batch(d["x"], w1, w2, 2, logits=logits, residual=d["residual"])
+    small1, small2 = w1[[0, e - 1]].contiguous(), w2[[0, e - 1]].contiguous()
+    want = ops.moe_layer_small_batch(d["x"], small1, small2, 2,
+                                     logits=logits[:, [0, e - 1]].contiguous(),
+                                     residual=d["residual"])
+    assert torch.equal(out, want)

@@ -126,6 +126,24 @@ def test_nan_and_infinity(cuda_device):
     assert torch.equal(w[[0, 3]], w2[[0, 3]]) and torch.equal(ids[[0, 3]], ids2[[0, 3]])
 
 
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("experts", [20, 64, 200, 400, 900])
+def test_nan_of_either_sign_and_infinities_by_type(cuda_device, dt, experts):
+    """NaN of either sign counts as the largest, whatever its bits; +inf comes next."""
+    z, _ = _logits(6, experts, dt, 21, cuda_device)
+    z[0, experts - 1] = float("nan")
+    z[1, 3] = -torch.tensor(float("nan"))
+    z[2, 5] = INF
+    z[3, 1] = INF
+    z[3, 7] = float("nan")
+    z[4, :] = -INF
+    z[4, 9] = -torch.tensor(float("nan"))
+    _, ids = ops.router_topk_fwd(z, 2, SIG, False)
+    assert ids[0, 0] == experts - 1 and ids[1, 0] == 3 and ids[2, 0] == 5
+    assert ids[3].tolist() == [7, 1] and ids[4].tolist() == [9, -1]
+    assert torch.equal(ids[5:], _choose(z[5:], 2))
+
+
 def _exact_grad(z, ids, gw, score, normalise, scale):
     with torch.enable_grad():
         z = z.double().requires_grad_()
