@@ -26,17 +26,16 @@ def moe_dtype(dtype: torch.dtype) -> int:
 def _cuda(*ts):
     """Every given tensor on one CUDA device (checked after the shape checks,
     just before the library call)."""
-    first = None
+    dev = None
     for t in ts:
         if t is None:
             continue
-        index = t.get_device()
-        if index < 0:
+        if not t.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
-        if first is None:
-            first, dev = t, index
-        elif index != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
 
 
 def _check(t, name, dtype=None, shape=None, numel=None, contiguous=True):
