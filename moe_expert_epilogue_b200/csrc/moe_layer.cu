@@ -465,9 +465,12 @@ struct Tile {
   static constexpr int kWeightBytes = T == kWide ? kRows * kCols * 2 : kRows * kPitch;
   static constexpr int kTokens = T == kWide ? kUnitTokens : T == kAny ? 2 * kNarrowTokens
                                                                       : kNarrowTokens;
-  // one buffer of the warps' sums; the ring: stages of weights, then up to 2 * most token rows
-  static constexpr int kRed = kConsumers * (kRows / 16) * 32 * 16;
-  static constexpr int kRing = (232448 - (int)sizeof(Tables) - 512 - 2 * kRed - 1024) / 1024 * 1024;
+  // one buffer of the warps' sums (of kWide there is one, and a barrier more: its place holds
+  // a third stage of units of 25 and more tokens); the ring: stages of weights, then up to
+  // 2 * most token rows
+  static constexpr int kRed = kConsumers * (kRows / 16) * 32 * 16, kReds = T == kWide ? 1 : 2;
+  static constexpr int kRing =
+      (232448 - (int)sizeof(Tables) - 512 - kReds * kRed - 1024) / 1024 * 1024;
 };
 
 static_assert(Tile<kWide>::kRing >= 2 * (Tile<kWide>::kWeightBytes +
@@ -892,7 +895,8 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j >= nt) break;
-      float4* r = red + buffer * (S::kRed / 16);
+      float4* r = red + (S::kReds == 1 ? 0 : buffer) * (S::kRed / 16);
+      if (S::kReds == 1) consumers_sync();             // the last sums have been read
 #pragma unroll
       for (int m = 0; m < M; ++m)
         r[(warp * M + m) * 32 + lane] =
@@ -1086,7 +1090,7 @@ int weight_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, i
 
 template <class D, Tiling T>
 int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t stream) {
-  constexpr size_t smem = Tile<T>::kRing + 2 * Tile<T>::kRed + 1024;
+  constexpr size_t smem = Tile<T>::kRing + Tile<T>::kReds * Tile<T>::kRed + 1024;
   if (int rc = ensure_smem_limit((const void*)layer_experts<D, T>, smem)) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
