@@ -300,3 +300,60 @@ def test_weights_feed_the_activation_and_gradients_come_back(cuda_device):
     want = _exact_grad(z, ids, (rows.double() * go.double()).sum(1).view(t, k), SOFT, True, 1.0)
     # grad_probs: 64 terms of order 1 summed in fp32, 1e-5 of a sum of order 50
     assert ((gl.double() - want).abs() <= 1e-4).all()
+
+
+def _sorted_choice(z, k):
+    """As _choose, for many tokens: a stable sort of the 64-bit values."""
+    v, i = z.double().sort(dim=1, descending=True, stable=True)
+    ids = torch.where(v[:, :k] == -INF, -1, i[:, :k]).int()
+    return torch.cat([ids, ids.new_full((ids.shape[0], k - ids.shape[1]), -1)], 1)
+
+
+@pytest.mark.parametrize("score,normalise,scale", MODES)
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("tokens,experts,top_k", [(4096, 8, 1), (4097, 64, 8), (5003, 161, 6),
+                                                  (16390, 256, 8), (4100, 40, 5), (4099, 1024, 7),
+                                                  (17001, 60, 3), (4098, 7, 7), (4101, 96, 9)])
+def test_many_tokens(cuda_device, tokens, experts, top_k, dt, score, normalise, scale):
+    """Many tokens, some of them closed or with fewer open experts than choices; each has the
+    bits that it has in a call of its own."""
+    z, _ = _logits(tokens, experts, dt, tokens, cuda_device, masked=0.3)
+    z[17] = -INF
+    z[tokens - 1, 1:] = -INF
+    w, ids = ops.router_topk_fwd(z, top_k, score, normalise, scale)
+    assert torch.equal(ids, _sorted_choice(z, top_k))
+    want = _weights(z, ids, score, normalise, scale)
+    live = ids >= 0
+    assert ((w.double() - want).abs() <= _tol(experts) * want.abs())[live].all()
+    assert (w[~live] == 0).all()
+    for a, b in ((0, 1), (16, 19), (40, 1040), (tokens - 70, tokens)):
+        ws, js = ops.router_topk_fwd(z[a:b], top_k, score, normalise, scale)
+        assert torch.equal(js, ids[a:b]) and torch.equal(ws, w[a:b])
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("experts", [56, 61, 256])
+def test_many_tokens_strides_valid_and_nan(cuda_device, dt, experts):
+    """Wider rows, rows off their alignment, NaN of either sign and zeros of either sign; tokens
+    past the count keep what was there."""
+    z, _ = _logits(4500, experts, dt, 29, cuda_device)
+    z[3, 5], z[4, 6], z[5, 2] = float("nan"), -float("nan"), INF
+    z[6] = 0.0
+    z[6, ::2] = -0.0
+    valid = torch.tensor([4497], dtype=torch.int32, device=cuda_device)
+    w, ids = ops.router_topk_fwd(z, 8)
+    assert ids[3, 0] == 5 and ids[4, 0] == 6 and ids[5, 0] == 2
+    assert ids[6].tolist() == list(range(8))
+    plain = torch.ones(4500, dtype=torch.bool, device=cuda_device)
+    plain[3:6] = False
+    assert torch.equal(ids[plain], _sorted_choice(z[plain], 8))
+    for wide, first in ((experts + 8, 0), (experts + 8, 8), (experts + 3, 1), (experts + 3, 3)):
+        row = torch.full((4500, wide), INF, dtype=dt, device=cuda_device)
+        row[:, first:first + experts] = z
+        w2 = torch.full_like(w, 7.0)
+        i2 = torch.full_like(ids, 7)
+        ops.router_topk_fwd(row[:, first:first + experts], 8, weights=w2, ids=i2,
+                            valid_tokens=valid)
+        assert torch.equal(i2[:4497], ids[:4497])
+        assert torch.equal(w2[:4497].view(torch.int32), w[:4497].view(torch.int32))
+        assert (w2[4497:] == 7).all() and (i2[4497:] == 7).all()
