@@ -1136,8 +1136,8 @@ int launch(const Layer& given, cudaStream_t stream) {
     return launch_experts<D, kAny>(a, maps, sms, stream);
   }
   // The narrow tiles' units hold 8 tokens: more tokens may need the weights again.  One token
-  // of eight 4096 x 2048 experts: 75 us in narrow tiles, 86 in wide ones; eight tokens of 64
-  // experts of 2048 x 512: 78 and 63.
+  // of eight 4096 x 2048 experts: 75 us in narrow tiles, 78 in wide ones; eight tokens of 64
+  // experts of 2048 x 512: 78 and 60.
   if ((a.tokens <= kNarrowTokens && tiles_time(a, 16, sms) <= tiles_time(a, 64, sms)) ||
       a.inter == 0)
     return launch_experts<D, kNarrow>(a, maps, sms, stream);

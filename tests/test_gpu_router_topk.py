@@ -357,3 +357,17 @@ def test_many_tokens_strides_valid_and_nan(cuda_device, dt, experts):
         assert torch.equal(i2[:4497], ids[:4497])
         assert torch.equal(w2[:4497].view(torch.int32), w[:4497].view(torch.int32))
         assert (w2[4497:] == 7).all() and (i2[4497:] == 7).all()
+
+
+@pytest.mark.parametrize("score,normalise,scale", MODES)
+@pytest.mark.parametrize("tokens,experts,top_k", [(1001, 64, 8), (333, 64, 9), (1003, 161, 6),
+                                                  (77, 256, 17), (35, 512, 16), (21, 128, 8)])
+def test_backward_bits_do_not_depend_on_the_batch(cuda_device, tokens, experts, top_k, score,
+                                                  normalise, scale):
+    z, g = _logits(tokens, experts, torch.float32, tokens, cuda_device, masked=0.2)
+    ids = ops.router_topk_fwd(z, top_k)[1]
+    gw = torch.randn(tokens, top_k, generator=g, device=cuda_device)
+    whole = ops.router_topk_bwd(z, ids, gw, score, normalise, scale)
+    for a, b in ((0, 1), (1, 4), (tokens - 5, tokens)):
+        part = ops.router_topk_bwd(z[a:b], ids[a:b], gw[a:b], score, normalise, scale)
+        assert torch.equal(part, whole[a:b])
