@@ -103,6 +103,7 @@ template <class D, int V> struct Sorted {                              // 16-bit
 template <int V> struct Sorted<F32, V> {
   uint32_t key[V];
   uint32_t at[V];                                                      // experts
+  static constexpr uint32_t kDead = kDeadKey;
   static constexpr bool kSort = V <= 8;     // beyond, sorting costs more than looking
   __device__ __forceinline__ void set(const float (&raw)[V], int E, int lane) {
 #pragma unroll
@@ -132,7 +133,7 @@ template <int V> struct Sorted<F32, V> {
       for (int i = 1; i < V; ++i) best = max(best, key[i]);
     }
     const uint32_t top = __reduce_max_sync(kAll, best);
-    if (top <= kDeadKey) return false;
+    if (top <= kDead) return false;
     if (kSort) {
       first = key[0] == top ? at[0] : ~0u;
     } else {
@@ -213,9 +214,16 @@ router_fwd(const typename D::T* __restrict__ logits, float* __restrict__ weights
 // larger of one list's i-th and the other's i-th from the end, then the end of a
 // bitonic sort); two or three such steps between the lanes leave every lane the
 // token's eight.  K <= 8.  A third of the instructions of the rounds above: 32768 x
-// 256 bf16, K = 8, 16.6 us there and 10.7 here.
+// 256, K = 8, bf16 16.6 us there and 10.7 here, fp32 24.2 and 16.8.
+// A key is a logit and its expert in one number: pair_key, and of fp32 the upper 22
+// bits of order_key with 0x3ff - expert (E <= 1024).  These order all but logits
+// that agree in 22 bits; so of fp32 the eight are ordered once more by their whole
+// logits, and a token whose ninth largest key shares the eighth's upper part is
+// chosen again, expert by expert.  (Keys of 64 bits: 32768 x 256 26.1 us.)
+template <bool NINTH>
 struct Eight {
   uint32_t key[8];                                                     // largest first
+  uint32_t ninth = 0;                                                  // largest left out
   __device__ __forceinline__ void order(int i, int j) {
     const uint32_t lo = min(key[i], key[j]);
     key[i] = max(key[i], key[j]);
@@ -233,7 +241,10 @@ struct Eight {
   }
   __device__ __forceinline__ void keep(const uint32_t (&other)[8]) {   // also largest first
 #pragma unroll
-    for (int i = 0; i < 8; ++i) key[i] = max(key[i], other[7 - i]);
+    for (int i = 0; i < 8; ++i) {
+      if (NINTH) ninth = max(ninth, min(key[i], other[7 - i]));
+      key[i] = max(key[i], other[7 - i]);
+    }
 #pragma unroll
     for (int o = 4; o > 0; o /= 2)
 #pragma unroll
@@ -252,16 +263,44 @@ __device__ __forceinline__ void pair_keys(uint32_t raw, uint32_t low, uint32_t& 
   k1 = __byte_perm(m, low, 0x3276);
 }
 
+// The eight choices of one fp32 token by the whole warp, in the order of (logit, expert).
+__device__ __forceinline__ void choose_again(const float* row, int E, int lane, uint32_t* key,
+                                             uint16_t* who) {
+  uint32_t last = ~0u, last_at = ~0u;
+  for (int k = 0; k < 8; ++k) {
+    uint32_t best = 0, at = ~0u;
+    for (int e = lane; e < E; e += 32) {
+      const uint32_t v = order_key(__ldg(row + e));
+      const bool left = v < last || (v == last && (k == 0 || (uint32_t)e > last_at));
+      if (left && v > best) {
+        best = v;
+        at = e;
+      }
+    }
+    last = __reduce_max_sync(kAll, best);
+    last_at = __reduce_min_sync(kAll, best == last ? at : ~0u);
+    if (lane == 0) {
+      key[k] = last;
+      who[k] = (uint16_t)last_at;
+    }
+  }
+}
+
 // LANES to a token; WIDE: rows of whole 16-byte words.
 template <class D, bool WIDE, int LANES>
 __global__ void __launch_bounds__(kThreads)
-router_fwd_many(const uint16_t* __restrict__ logits, float* __restrict__ weights,
+router_fwd_many(const typename D::T* __restrict__ logits, float* __restrict__ weights,
                 int32_t* __restrict__ ids, const int32_t* __restrict__ valid, int64_t tokens,
                 int E, int K, int lanes, int64_t ld, bool softmax, bool normalise, float scale,
                 int32_t* err) {
-  constexpr uint32_t kClosed = std::is_same<D, BF16>::value ? 0xff80ff80u : 0xfc00fc00u;  // -inf
+  constexpr bool kHalf = D::kBytes == 2;
+  constexpr int kWords = 2 * D::kBytes;                                // of eight logits
+  constexpr uint32_t kClosed =                                         // a word of -inf
+      std::is_same<D, BF16>::value ? 0xff80ff80u : kHalf ? 0xfc00fc00u : 0xff800000u;
+  constexpr uint32_t kDead = Sorted<D, 1>::kDead;
   constexpr int kWarpTokens = 32 / LANES;
-  __shared__ __align__(16) uint32_t chosen[kThreads / 32][kWarpTokens][8];
+  __shared__ uint32_t chosen[kThreads / 32][kWarpTokens][8];
+  __shared__ uint16_t who[kThreads / 32][kWarpTokens][kHalf ? 1 : 8];  // of fp32: the experts
   __shared__ float sums[kThreads / 32][kWarpTokens];
   pdl_prologue();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -270,39 +309,50 @@ router_fwd_many(const uint16_t* __restrict__ logits, float* __restrict__ weights
   for (int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * kWarpTokens; t0 < n;
        t0 += step) {
     const int64_t t = t0 + lane / LANES;
-    const uint16_t* row = logits + t * ld;
-    const auto load = [&](int e, uint32_t (&raw)[4]) {
-      raw[0] = raw[1] = raw[2] = raw[3] = kClosed;
+    const typename D::T* row = logits + t * ld;
+    const auto load = [&](int e, uint32_t (&raw)[kWords]) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) raw[i] = kClosed;
       if (t >= n) return;
-      if (WIDE) {
+      if constexpr (WIDE) {
         if (e < E) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e));
-          raw[0] = v.x; raw[1] = v.y; raw[2] = v.z; raw[3] = v.w;
+#pragma unroll
+          for (int i = 0; i < kWords; i += 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e) + i / 4);
+            raw[i] = v.x; raw[i + 1] = v.y; raw[i + 2] = v.z; raw[i + 3] = v.w;
+          }
         }
-      } else {
+      } else if constexpr (kHalf) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t a = e + 2 * i < E ? __ldg(row + e + 2 * i) : kClosed & 0xffffu;
           const uint32_t b = e + 2 * i + 1 < E ? __ldg(row + e + 2 * i + 1) : kClosed & 0xffffu;
           raw[i] = a | b << 16;
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e + i < E) raw[i] = __float_as_uint(__ldg(row + e + i));
       }
     };
-    Eight top = {};
+    Eight<!kHalf> top;
     int e = (lane & (LANES - 1)) * 8;
-    uint32_t next[4];
+    uint32_t next[kWords];
     load(e, next);
     for (int e0 = 0; e0 < E; e0 += 8 * LANES, e += 8 * LANES) {
-      uint32_t raw[4];
+      Eight<!kHalf> some;
+      if constexpr (kHalf) {
+        // the lower half of a key: 0xffff - expert
+        const uint32_t low = (0xffffu - e) | (0xfffeu - e) << 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = next[i];
+        for (int i = 0; i < 4; ++i)
+          pair_keys<D>(next[i], low - i * 0x00020002u, some.key[2 * i], some.key[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          some.key[i] = (order_key(__uint_as_float(next[i])) & ~0x3ffu) | (~(e + i) & 0x3ff);
+      }
       if (e0 + 8 * LANES < E) load(e + 8 * LANES, next);
-      Eight some;
-      // the lower half of a key: 0xffff - expert
-      const uint32_t low = (0xffffu - e) | (0xfffeu - e) << 16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pair_keys<D>(raw[i], low - i * 0x00020002u, some.key[2 * i], some.key[2 * i + 1]);
       some.sort();
       if (e0 == 0) top = some;
       else top.keep(some.key);
@@ -312,24 +362,54 @@ router_fwd_many(const uint16_t* __restrict__ logits, float* __restrict__ weights
       uint32_t other[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, top.key[i], o);
+      if (!kHalf) top.ninth = max(top.ninth, __shfl_xor_sync(kAll, top.ninth, o));
       top.keep(other);
     }
     if ((lane & (LANES - 1)) == 0) {
-      uint4* to = reinterpret_cast<uint4*>(chosen[warp][lane / LANES]);
-      to[0] = make_uint4(top.key[0], top.key[1], top.key[2], top.key[3]);
-      to[1] = make_uint4(top.key[4], top.key[5], top.key[6], top.key[7]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) chosen[warp][lane / LANES][i] = top.key[i];
     }
     __syncwarp();
+    if constexpr (!kHalf) {
+#pragma unroll
+      for (int at = lane; at < 8 * kWarpTokens; at += 32) {
+        const int g = at / 8, k = at & 7;
+        const uint32_t key = chosen[warp][g][k], expert = ~key & 0x3ffu;
+        const uint32_t whole =
+            key > kDead ? order_key(__ldg(logits + (t0 + g) * ld + expert)) : 0u;
+        int place = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t v = __shfl_sync(kAll, whole, j, 8);
+          place += v > whole || (v == whole && j < k);       // equal ones are in order already
+        }
+        __syncwarp();
+        chosen[warp][g][place] = whole;
+        who[warp][g][place] = (uint16_t)expert;
+      }
+      const bool unsure = top.key[7] > kDead && top.ninth >> 10 == top.key[7] >> 10;
+      uint32_t tokens_left = __ballot_sync(kAll, unsure && (lane & (LANES - 1)) == 0);
+      __syncwarp();
+      for (; tokens_left; tokens_left &= tokens_left - 1) {
+        const int g = (__ffs(tokens_left) - 1) / LANES;
+        choose_again(logits + (t0 + g) * ld, E, lane, chosen[warp][g], who[warp][g]);
+      }
+      __syncwarp();
+    }
+    const auto value = [&](uint32_t key) {
+      if constexpr (kHalf) return pair_value<D>(key);
+      else return key_value(key);
+    };
     if (softmax && !normalise) {
       // as exp_sum, four tokens at a time; a token past the last repeats it
       for (int g0 = 0; g0 < kWarpTokens && t0 + g0 < n; g0 += 4) {
-        const uint16_t* from[4];
+        const typename D::T* from[4];
         float first[4], s[4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int g = t0 + g0 + j < n ? g0 + j : g0;
           from[j] = logits + (t0 + g) * ld;
-          first[j] = pair_value<D>(chosen[warp][g][0]);
+          first[j] = value(chosen[warp][g][0]);
         }
         for (int i = lane; i < E; i += 32) {
 #pragma unroll
@@ -349,11 +429,12 @@ router_fwd_many(const uint16_t* __restrict__ logits, float* __restrict__ weights
       const int g = at / lanes, k = at & (lanes - 1);
       const bool mine = g < kWarpTokens && k < K && t0 + g < n;
       const uint32_t key = mine ? chosen[warp][g][k] : 0u;
-      const bool some = key > Sorted<D, 1>::kDead;
-      const int id = some ? 0xffff - (int)(key & 0xffffu) : -1;
+      const bool some = key > kDead;
+      int id = -1;
+      if (some) id = kHalf ? 0xffff - (int)(key & 0xffffu) : who[warp][g][kHalf ? 0 : k];
       const float all = softmax && !normalise && mine ? sums[warp][g] : 1.0f;
-      const float w = choice_weight(some ? pair_value<D>(key) : -kInf, id, lanes, lane, softmax,
-                                    normalise, scale, all);
+      const float w = choice_weight(some ? value(key) : -kInf, id, lanes, lane, softmax, normalise,
+                                    scale, all);
       if (mine) {
         weights[(t0 + g) * K + k] = w;
         ids[(t0 + g) * K + k] = id;
@@ -470,27 +551,28 @@ int launch_fwd(const void* logits, float* weights, int32_t* ids, const int32_t* 
                float scale, int32_t* err, cudaStream_t stream) {
   int lanes = 1, grid = 0;
   while (lanes < K) lanes *= 2;
-  if constexpr (!std::is_same<D, F32>::value) {
-    // Fewer tokens leave its warps waiting for themselves (2048 x 256 bf16: 2.8 us a token a
-    // warp, 3.1 with eight lanes to a token; 4096: 4.0 and 3.2).  Four lanes need fewer steps
-    // between lanes, eight more of them at once (16384 x 256: 6.6 us both, 32768: 10.7 with four,
-    // 11.9 with eight), and the sums over all experts wait less with fewer tokens a warp
-    // (32768: 19.0 and 18.0).
-    if (K <= 8 && tokens >= 4096) {
-      const bool wide = ((reinterpret_cast<uintptr_t>(logits) & 15) | (ld & 7) | (E & 7)) == 0;
-      const bool four = tokens > 16384 && !(softmax && !normalise);
-      const auto k = four ? wide ? router_fwd_many<D, true, 4> : router_fwd_many<D, false, 4>
-                          : wide ? router_fwd_many<D, true, 8> : router_fwd_many<D, false, 8>;
-      const int64_t per = kThreads / (four ? 4 : 8);
-      if (int rc = persistent_grid((const void*)k, 0, (tokens + per - 1) / per, &grid)) return rc;
-      launch_kernel(k, grid, 0, stream, static_cast<const uint16_t*>(logits), weights, ids, valid,
-                    tokens, E, K, lanes, ld, softmax, normalise, scale, err);
-      return check_launch();
-    }
+  // Fewer tokens leave its warps waiting for themselves (2048 x 256 bf16: 2.8 us a token a
+  // warp, 3.1 with eight lanes to a token; 4096: 4.0 and 3.2; fp32 4096: 5.0 and 5.9, 8192: 8.2 and
+  // 7.5).  Four lanes need fewer steps between lanes, eight more of them at once (16384 x 256:
+  // 6.6 us both, 32768: 10.7 with four, 11.9 with eight), and the sums over all experts wait less
+  // with fewer tokens a warp (32768: 19.0 and 18.0), as do the second looks of fp32 (18.2 and
+  // 16.8).
+  constexpr bool kHalf = D::kBytes == 2;
+  if (K <= 8 && tokens >= (kHalf ? 4096 : 8192)) {
+    const bool wide =
+        ((reinterpret_cast<uintptr_t>(logits) & 15) | (ld * D::kBytes & 15) | (E & 7)) == 0;
+    const bool four = kHalf && tokens > 16384 && !(softmax && !normalise);
+    constexpr int kFour = kHalf ? 4 : 8;
+    const auto k = four ? wide ? router_fwd_many<D, true, kFour> : router_fwd_many<D, false, kFour>
+                        : wide ? router_fwd_many<D, true, 8> : router_fwd_many<D, false, 8>;
+    const int64_t per = kThreads / (four ? 4 : 8);
+    if (int rc = persistent_grid((const void*)k, 0, (tokens + per - 1) / per, &grid)) return rc;
+    launch_kernel(k, grid, 0, stream, static_cast<const typename D::T*>(logits), weights, ids,
+                  valid, tokens, E, K, lanes, ld, softmax, normalise, scale, err);
+    return check_launch();
   }
   auto k = router_fwd<D, V>;
-  // one token a warp as long as there are warps for them, which is quicker for each token (K > 8
-  // or fp32)
+  // one token a warp as long as there are warps for them, which is quicker for each token (K > 8)
   const int group = tokens > 16384 ? 32 / lanes : 1;
   const int64_t per = (int64_t)(kThreads / 32) * group;
   if (int rc = persistent_grid((const void*)k, 0, (tokens + per - 1) / per, &grid)) return rc;

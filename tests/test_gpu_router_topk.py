@@ -313,7 +313,9 @@ def _sorted_choice(z, k):
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("tokens,experts,top_k", [(4096, 8, 1), (4097, 64, 8), (5003, 161, 6),
                                                   (16390, 256, 8), (4100, 40, 5), (4099, 1024, 7),
-                                                  (17001, 60, 3), (4098, 7, 7), (4101, 96, 9)])
+                                                  (17001, 60, 3), (4098, 7, 7), (4101, 96, 9),
+                                                  (8203, 161, 6), (8192, 8, 1), (8199, 1024, 8),
+                                                  (8198, 7, 7)])
 def test_many_tokens(cuda_device, tokens, experts, top_k, dt, score, normalise, scale):
     """Many tokens, some of them closed or with fewer open experts than choices; each has the
     bits that it has in a call of its own."""
@@ -333,30 +335,32 @@ def test_many_tokens(cuda_device, tokens, experts, top_k, dt, score, normalise, 
 
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("experts", [56, 61, 256])
-def test_many_tokens_strides_valid_and_nan(cuda_device, dt, experts):
+@pytest.mark.parametrize("tokens", [4500, 8500])
+def test_many_tokens_strides_valid_and_nan(cuda_device, tokens, dt, experts):
     """Wider rows, rows off their alignment, NaN of either sign and zeros of either sign; tokens
     past the count keep what was there."""
-    z, _ = _logits(4500, experts, dt, 29, cuda_device)
+    last = tokens - 3
+    z, _ = _logits(tokens, experts, dt, 29, cuda_device)
     z[3, 5], z[4, 6], z[5, 2] = float("nan"), -float("nan"), INF
     z[6] = 0.0
     z[6, ::2] = -0.0
-    valid = torch.tensor([4497], dtype=torch.int32, device=cuda_device)
+    valid = torch.tensor([last], dtype=torch.int32, device=cuda_device)
     w, ids = ops.router_topk_fwd(z, 8)
     assert ids[3, 0] == 5 and ids[4, 0] == 6 and ids[5, 0] == 2
     assert ids[6].tolist() == list(range(8))
-    plain = torch.ones(4500, dtype=torch.bool, device=cuda_device)
+    plain = torch.ones(tokens, dtype=torch.bool, device=cuda_device)
     plain[3:6] = False
     assert torch.equal(ids[plain], _sorted_choice(z[plain], 8))
     for wide, first in ((experts + 8, 0), (experts + 8, 8), (experts + 3, 1), (experts + 3, 3)):
-        row = torch.full((4500, wide), INF, dtype=dt, device=cuda_device)
+        row = torch.full((tokens, wide), INF, dtype=dt, device=cuda_device)
         row[:, first:first + experts] = z
         w2 = torch.full_like(w, 7.0)
         i2 = torch.full_like(ids, 7)
         ops.router_topk_fwd(row[:, first:first + experts], 8, weights=w2, ids=i2,
                             valid_tokens=valid)
-        assert torch.equal(i2[:4497], ids[:4497])
-        assert torch.equal(w2[:4497].view(torch.int32), w[:4497].view(torch.int32))
-        assert (w2[4497:] == 7).all() and (i2[4497:] == 7).all()
+        assert torch.equal(i2[:last], ids[:last])
+        assert torch.equal(w2[:last].view(torch.int32), w[:last].view(torch.int32))
+        assert (w2[last:] == 7).all() and (i2[last:] == 7).all()
 
 
 @pytest.mark.parametrize("score,normalise,scale", MODES)
@@ -371,3 +375,24 @@ def test_backward_bits_do_not_depend_on_the_batch(cuda_device, tokens, experts, 
     for a, b in ((0, 1), (1, 4), (tokens - 5, tokens)):
         part = ops.router_topk_bwd(z[a:b], ids[a:b], gw[a:b], score, normalise, scale)
         assert torch.equal(part, whole[a:b])
+
+
+@pytest.mark.parametrize("score,normalise,scale", MODES)
+@pytest.mark.parametrize("tokens,experts,top_k", [(8199, 64, 8), (17000, 256, 8), (9000, 61, 3),
+                                                  (8192, 1024, 8), (8192, 7, 7)])
+def test_many_tokens_with_close_logits(cuda_device, tokens, experts, top_k, score, normalise,
+                                       scale):
+    """fp32 logits that differ in their last bits only, many of them equal, of either sign."""
+    g = torch.Generator(device=cuda_device).manual_seed(tokens)
+    z = 1.0 + torch.randint(0, 900, (tokens, experts), generator=g, device=cuda_device) * 2.0 ** -23
+    z[::3] = -z[::3]
+    z[1::5, ::2] = -INF
+    z[7] = 0.0
+    z[8, 1::2] = 0.5
+    w, ids = ops.router_topk_fwd(z, top_k, score, normalise, scale)
+    assert torch.equal(ids, _sorted_choice(z, top_k))
+    want = _weights(z, ids, score, normalise, scale)
+    live = ids >= 0
+    assert ((w.double() - want).abs() <= _tol(experts) * want.abs())[live].all()
+    ws, js = ops.router_topk_fwd(z[30:70], top_k, score, normalise, scale)
+    assert torch.equal(js, ids[30:70]) and torch.equal(ws, w[30:70])
