@@ -337,7 +337,7 @@ router_fwd_many(const typename D::T* __restrict__ logits, float* __restrict__ we
     };
     Eight<!kHalf> top;
     int e = (lane & (LANES - 1)) * 8;
-    uint32_t next[kWords];
+    uint32_t next[kWords], bits = 0;
     load(e, next);
     for (int e0 = 0; e0 < E; e0 += 8 * LANES, e += 8 * LANES) {
       Eight<!kHalf> some;
@@ -349,8 +349,10 @@ router_fwd_many(const typename D::T* __restrict__ logits, float* __restrict__ we
           pair_keys<D>(next[i], low - i * 0x00020002u, some.key[2 * i], some.key[2 * i + 1]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+          bits |= next[i];
           some.key[i] = (order_key(__uint_as_float(next[i])) & ~0x3ffu) | (~(e + i) & 0x3ff);
+        }
       }
       if (e0 + 8 * LANES < E) load(e + 8 * LANES, next);
       some.sort();
@@ -362,7 +364,10 @@ router_fwd_many(const typename D::T* __restrict__ logits, float* __restrict__ we
       uint32_t other[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, top.key[i], o);
-      if (!kHalf) top.ninth = max(top.ninth, __shfl_xor_sync(kAll, top.ninth, o));
+      if (!kHalf) {
+        top.ninth = max(top.ninth, __shfl_xor_sync(kAll, top.ninth, o));
+        bits |= __shfl_xor_sync(kAll, bits, o);
+      }
       top.keep(other);
     }
     if ((lane & (LANES - 1)) == 0) {
@@ -387,7 +392,9 @@ router_fwd_many(const typename D::T* __restrict__ logits, float* __restrict__ we
         chosen[warp][g][place] = whole;
         who[warp][g][place] = (uint16_t)expert;
       }
-      const bool unsure = top.key[7] > kDead && top.ninth >> 10 == top.key[7] >> 10;
+      // (of logits without lower bits, say from a 16-bit type, the keys hold all)
+      const bool unsure =
+          top.key[7] > kDead && top.ninth >> 10 == top.key[7] >> 10 && (bits & 0x3ffu);
       uint32_t tokens_left = __ballot_sync(kAll, unsure && (lane & (LANES - 1)) == 0);
       __syncwarp();
       for (; tokens_left; tokens_left &= tokens_left - 1) {
