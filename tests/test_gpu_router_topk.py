@@ -396,3 +396,25 @@ def test_many_tokens_with_close_logits(cuda_device, tokens, experts, top_k, scor
     assert ((w.double() - want).abs() <= _tol(experts) * want.abs())[live].all()
     ws, js = ops.router_topk_fwd(z[30:70], top_k, score, normalise, scale)
     assert torch.equal(js, ids[30:70]) and torch.equal(ws, w[30:70])
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("experts", [24, 65])
+def test_many_tokens_of_extreme_values(cuda_device, dt, experts):
+    """The type's lowest and largest values, subnormal ones and zeros, among closed experts."""
+    info = torch.finfo(dt)
+    least = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -24, torch.float32: 2.0 ** -149}[dt]
+    values = torch.tensor([info.min, info.max, info.tiny, -info.tiny, least, -least, 3 * least, 0.0,
+                           -0.0, -INF, INF], dtype=dt, device=cuda_device)
+    g = torch.Generator(device=cuda_device).manual_seed(experts)
+    z = values[torch.randint(0, values.numel(), (8200, experts), generator=g, device=cuda_device)]
+    z[5] = info.min
+    z[6] = -INF
+    z[6, 3::7] = info.min
+    ids = ops.router_topk_fwd(z, 8)[1]
+    assert torch.equal(ids, _sorted_choice(z, 8))
+    for a, b in ((0, 40), (8190, 8200)):
+        assert torch.equal(ops.router_topk_fwd(z[a:b], 8)[1], ids[a:b])
+    w = ops.router_topk_fwd(z, 8, SIG, False)[0]
+    want = torch.sigmoid(z.double().gather(1, ids.long().clamp(min=0))) * (ids >= 0)
+    assert ((w.double() - want).abs() <= 8 * U * want + 2.0 ** -126).all()
