@@ -606,6 +606,30 @@ MOE_API int moe_test_swiglu_fwd_stalled(const void* x, const float* probs, void*
                                         int32_t* dev_err, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Test hook of the few-token layer's bounded waits (not for production use).
+ * moe_layer_small_batch of contiguous bf16 tensors and fp32 logits (softmax over
+ * the chosen experts, no limit, no shared expert, no residual), in which the
+ * first CTA withholds what `stall` names and every wait gives up after
+ * `wait_cycles` SM cycles.  The kernel ends by itself: once a wait of a CTA has
+ * given up, its producers fill nothing more and the CTA waits (as long again at
+ * most) for the copies that it issued.  *dev_err receives MOE_DEVERR_TIMEOUT, the results are
+ * void, the workspace can be used again and the CUDA context stays usable.
+ * stall     0, 1: the copy of the CTA's third stage of weights in the first,
+ *           second product; 2: a third of the third stage's tokens in both;
+ *           3, 4, 5: its arrival at the grid barrier after the choice (calls of more than 24
+ *           tokens), between the products, before the combine
+ * wait_cycles  1000 .. 2^31
+ * tokens, hidden, inter at least 1;  dev_err required (MOE_ERR_NULL)
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_test_layer_small_batch_stalled(const void* x, const float* logits, const void* w1,
+                                               const void* w2, void* out, void* workspace,
+                                               int64_t workspace_bytes, int64_t tokens,
+                                               int64_t hidden, int64_t inter,
+                                               int32_t num_experts, int32_t top_k, int32_t stall,
+                                               int64_t wait_cycles, int32_t* dev_err,
+                                               cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Buffers shared between the processes of one node (CUDA IPC): the plumbing
  * under moe_ordered_reduce_scatter_v's `buffers` (the pages use a symmetric-
  * memory handle; this library maps plain device allocations instead).

@@ -56,6 +56,8 @@ SIGNATURES = {
     "moe_layer_small_batch": [_P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
                               _I64, _I64, _I64, _I32, _I32, _I64, _I64, _I64, _I64, _I64, _I, _I,
                               _F, _F, _P, _P],
+    "moe_test_layer_small_batch_stalled": [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32,
+                                           _I32, _I32, _I64, _P, _P],
     "moe_symm_alloc": [ctypes.c_size_t, ctypes.POINTER(_P)],
     "moe_symm_free": [_P],
     "moe_ipc_export": [_P, ctypes.c_char_p],
@@ -303,6 +305,15 @@ def moe_layer_small_batch(x, dt, router_weight, router_dt, logits, logits_dt, w1
           tokens, hidden, inter, num_experts, top_k, ld_x, ld_logits, ld_shared, ld_residual,
           ld_out, score, int(bool(normalise)), float(scale), float(limit), ptr(dev_err),
           stream_handle(stream))
+
+
+def moe_test_layer_small_batch_stalled(x, logits, w1, w2, out, workspace, workspace_bytes, tokens,
+                                       hidden, inter, num_experts, top_k, stall, wait_cycles,
+                                       dev_err, stream=None):
+    """The few-token layer with something withheld that its waits wait for (tests)."""
+    _call("moe_test_layer_small_batch_stalled", ptr(x), ptr(logits), ptr(w1), ptr(w2), ptr(out),
+          ptr(workspace), workspace_bytes, tokens, hidden, inter, num_experts, top_k, stall,
+          wait_cycles, ptr(dev_err), stream_handle(stream))
 
 
 def moe_symm_alloc(nbytes: int) -> int:

@@ -587,4 +587,31 @@ int moe_layer_small_batch(const void* x, moe_dtype dt, const void* router_weight
   return launch_moe_layer(m, stream);
 }
 
+int moe_test_layer_small_batch_stalled(const void* x, const float* logits, const void* w1,
+                                       const void* w2, void* out, void* workspace,
+                                       int64_t workspace_bytes, int64_t tokens, int64_t hidden,
+                                       int64_t inter, int32_t num_experts, int32_t top_k,
+                                       int32_t stall, int64_t wait_cycles, int32_t* dev_err,
+                                       cudaStream_t stream) {
+  if (!moe_layer_shape_ok(tokens, hidden, inter, num_experts, top_k) || tokens < 1 ||
+      hidden < 1 || inter < 1 || !moe_layer_stall_ok(stall) || wait_cycles < 1000 ||
+      wait_cycles > tma::kWaitCycles ||
+      workspace_bytes < moe_layer_workspace(tokens, hidden, inter, num_experts, top_k))
+    return MOE_ERR_SHAPE;
+  if (!x || !logits || !w1 || !w2 || !out || !workspace || !dev_err) return MOE_ERR_NULL;
+  if (!aligned_to(x, 2) || !aligned_to(w1, 2) || !aligned_to(w2, 2) || !aligned_to(out, 2) ||
+      !aligned_to(logits, 4) || !aligned_to(dev_err, 4) || !aligned_to(workspace, 256))
+    return MOE_ERR_ALIGN;
+  MoeLayerArgs m = {};
+  m.x = x; m.logits = logits; m.w1 = w1; m.w2 = w2; m.out = out; m.workspace = workspace;
+  m.tokens = (int)tokens; m.hidden = (int)hidden; m.inter = (int)inter;
+  m.E = num_experts; m.K = top_k;
+  m.ld_x = m.ld_out = hidden; m.ld_logits = num_experts;
+  m.dt = MOE_BF16; m.router_dt = m.logits_dt = MOE_FP32;
+  m.softmax = m.normalise = true;
+  m.scale = 1.0f; m.limit = INFINITY; m.err = dev_err;
+  m.stall = stall; m.wait_cycles = wait_cycles;
+  return launch_moe_layer(m, stream);
+}
+
 }  // extern "C"

@@ -156,9 +156,12 @@ struct MoeLayerArgs {
   bool softmax, normalise;
   float scale, limit;
   int32_t* err;
+  int stall;               // tests of the bounded waits: what is withheld,
+  long long wait_cycles;   // and their limit (0: an ordinary call)
 };
 // Copies (and optionally clears) the few-token layer's per-device timeout word.
 int moe_layer_device_errors(int32_t* bits, int clear);
+bool moe_layer_stall_ok(int stall);
 bool moe_layer_shape_ok(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K);
 int64_t moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t E, int64_t K);
 int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream);

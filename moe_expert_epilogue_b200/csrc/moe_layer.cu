@@ -94,6 +94,8 @@ struct Layer {
   bool eights;           // shared, residual and out in 16-byte pieces
   float scale, limit;
   int32_t* err;
+  int stall;             // tests of the waits (STALLED kernels): what is withheld, and the limit
+  long long wait_cycles;
   // workspace
   unsigned* barrier;     // [kBarriers]
   uint16_t* padded_x;    // kAny: [tokens, hidden up to a multiple of 8], else null
@@ -218,26 +220,41 @@ void launch_logits(const Layer& a, cudaStream_t stream) {
 
 // ------------------------------------------------------------ waits
 
-// Every wait gives up after kWaitCycles: the waiter reports it and sets the
-// CTA's flag, and from then on nobody in the CTA waits, so that the kernel runs
-// to its end (its results are void) with every CTA barrier met.
+// Every wait gives up after `limit` cycles (kWaitCycles): the waiter reports it
+// and sets the CTA's flag.  From then on nobody in the CTA waits, so that the
+// kernel runs to its end (its results are void) with every CTA barrier met; the
+// producers end at the next stage that they cannot have (Slot).
 
 struct GiveUp {
   volatile int* flag;   // shared memory
   int32_t* err;
+  long long limit;
   __device__ __forceinline__ bool now(long long t0) const {
     if (*flag) return true;
-    if (clock64() - t0 <= tma::kWaitCycles) return false;
+    if (clock64() - t0 <= limit) return false;
     *flag = 1;
     flag_error(err, MOE_DEVERR_TIMEOUT);
     return true;
   }
 };
 
-__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, const GiveUp& g) {
-  if (tma::mbar_try(bar, parity)) return;
+// What a STALLED kernel (tests of the waits) withholds in its first CTA: the third
+// fill of a producer, or an arrival at the grid barrier kStallBarrier + i.
+enum Stall { kStallWeights1 = 0, kStallWeights2, kStallTokens, kStallBarrier };
+constexpr int kStalls = kStallBarrier + kBarriers;
+
+template <bool STALLED>
+__device__ __forceinline__ bool withheld(const Layer& a, int what) {
+  return STALLED && blockIdx.x == 0 && a.stall == what;
+}
+
+// Whether the phase was seen complete.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const GiveUp& g) {
+  if (tma::mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!tma::mbar_try(bar, parity) && !g.now(t0)) {}
+  while (!tma::mbar_try(bar, parity))
+    if (g.now(t0)) return false;
+  return true;
 }
 
 // Grid barrier, in two parts.  The launch is cooperative: all CTAs are resident.
@@ -318,6 +335,7 @@ __device__ __forceinline__ void choose(const Layer& a, int t, int step, int live
 //   A choice takes a warp about 2 us.  Up to two tokens a warp every CTA makes
 // them all; more are shared among the CTAs, at the price of a grid barrier (64
 // tokens of 64 experts: 12 us down to 5).
+template <bool STALLED>
 __device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int unit_tokens,
                             int threads, const GiveUp& g) {
   constexpr int kWords = kMaxTokens / 32;
@@ -350,7 +368,7 @@ __device__ void make_tables(const Layer& a, Tables& tb, uint32_t* chosen, int un
       });
       __syncwarp();
       if (lane == 0) {
-        grid_arrive(&a.barrier[0]);
+        if (!withheld<STALLED>(a, kStallBarrier)) grid_arrive(&a.barrier[0]);
         grid_wait(&a.barrier[0], g);
       }
     }
@@ -484,22 +502,63 @@ static_assert(Tile<kWide>::kRing >= kMaxLayerExperts * (kMaxTokens / 32) * 4,
 struct Ring {
   uint8_t* base;         // 1024-byte aligned
   uint64_t *full, *empty;
+  volatile int* filled;  // the stages of weights, once their producer has ended; before: -1
   int stage_bytes, stages;
 };
+
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Whose slots: of the tokens' producers, of the weights' (kWide: the first lane issues all
+// copies; else every lane its row's).
+enum Producer { kTokens, kBoxes, kRows };
 
 // A place in the ring: the slot and the parity of its current use.
 struct Slot {
   int at = 0;
-  uint32_t parity = 0;
-  int fresh;             // slots not used yet
-  __device__ explicit Slot(const Ring& r) : fresh(r.stages) {}
+  uint32_t parity = 0;   // bit 1, of a consumer: a wait gave up
+  int uses = 0;          // of the ring before this one
   __device__ __forceinline__ void next(const Ring& r) {
+    ++uses;
     if (++at == r.stages) { at = 0; parity ^= 1u; }
   }
-  // Waits until the slot may be overwritten.
-  __device__ __forceinline__ void claim(const Ring& r, const GiveUp& g) {
-    if (fresh > 0) --fresh;
-    else wait_phase(&r.empty[at], parity ^ 1u, g);
+  // Consumers: waits until the slot has been filled.  One that gave up releases no slot any more.
+  __device__ __forceinline__ void wait(const Ring& r, const GiveUp& g) {
+    if (!wait_phase(&r.full[at], parity & 1u, g)) parity |= 2u;
+  }
+  __device__ __forceinline__ bool dead() const { return parity > 1u; }
+
+  // How the producers end, in order or where a wait has given up.  As consumers that gave up
+  // release nothing, a slot is only had if the fill before it has landed: the barriers' phases
+  // follow the fills, and their counts of bytes stay small.  A producer that does not get its
+  // slot ends there (of the tokens', each lane for itself).  The weights' first lane says how
+  // many stages have been filled, and waits until they have landed, as a CTA does not end before
+  // its copies; a lane of the tokens' that stopped earlier makes up for its arrivals at these.
+  __device__ __forceinline__ void end_weights(const Ring& r, const GiveUp& g) const {
+    *r.filled = uses;
+    for (int i = 0; i < min(uses, r.stages); ++i)
+      if (!tma::mbar_wait(&r.full[i], i < at ? parity : parity ^ 1u, g.limit))
+        flag_error(g.err, MOE_DEVERR_TIMEOUT);
+  }
+  __device__ __forceinline__ void end_tokens(const Ring& r) {
+    const long long t0 = clock64();
+    // (said as soon as the weights' producer meets a slot that it has to wait for)
+    while (*r.filled < 0 && clock64() - t0 <= tma::kWaitCycles) {}
+    for (; uses < *r.filled; next(r)) tma::mbar_arrive(&r.full[at]);
+    cp_async_wait();
+  }
+  // Producers: waits until the slot may be overwritten.  (One token of 4096 x 2048 experts 75.8
+  // us, 128 tokens 712; where it returns that the slot may not be had, and the callers' loops are
+  // left by a branch, 77 to 83 and 730 to 767.)
+  template <Producer P>
+  __device__ __forceinline__ void claim(const Ring& r, const GiveUp& g, int lane) {
+    const bool had = uses < r.stages || wait_phase(&r.empty[at], parity ^ 1u, g);
+    if (P == kRows ? __all_sync(kAll, had) : had) return;
+    if (P == kTokens) end_tokens(r);
+    else if (lane == 0) end_weights(r, g);
+    asm volatile("exit;");
+    __builtin_unreachable();
   }
 };
 
@@ -568,19 +627,23 @@ __device__ __forceinline__ const uint16_t* weight_row(const Layer& a, int expert
          (((int64_t)expert * 2 + (r >> 3)) * a.inter + j) * a.hidden;
 }
 
-template <Tiling T, bool SECOND>
+template <Tiling T, bool SECOND, bool STALLED>
 __device__ __forceinline__ void produce_weights(const Layer& a, const WeightMaps& maps,
                                                 const Tables& tb, const Ring& ring, Slot& slot,
                                                 const GiveUp& g, int lane) {
   using S = Tile<T>;
+  int fills = 0;
   for_stages<T>(tb, make_product<T, SECOND>(a, tb), [&](Unit u, int tile, int k0, int len) {
-    slot.claim(ring, g);
+    const bool hold = STALLED && fills++ == 2 &&
+                      withheld<STALLED>(a, SECOND ? kStallWeights2 : kStallWeights1);
+    // (what does not need the slot comes before the wait for it)
     uint8_t* stage = ring.base + (size_t)slot.at * ring.stage_bytes;
     uint64_t* full = &ring.full[slot.at];
     if (T == kWide) {
       // 64-column boxes of 64 rows (first product: 32 gate rows, 32 up rows)
       const int boxes = (len + 63) / 64;
-      if (lane == 0) {
+      slot.claim<kBoxes>(ring, g, lane);
+      if (lane == 0 && !hold) {
         tma::mbar_arrive_expect_tx(full, boxes * 8192);
         for (int b = 0; b < boxes; ++b) {
           if (SECOND) {
@@ -595,8 +658,9 @@ __device__ __forceinline__ void produce_weights(const Layer& a, const WeightMaps
     } else {
       const uint16_t* src = lane < 16 ? weight_row<SECOND>(a, u.expert, tile, lane) : nullptr;
       uint8_t* dst = stage + lane * S::kPitch;
-      uint32_t bytes = src ? len * 2 : 0;
+      uint32_t bytes = src && !hold ? len * 2 : 0;
       if (src) src += k0;
+      slot.claim<kRows>(ring, g, lane);
       if (T == kAny) {
         // the 16-byte words that hold the row, unless they reach past the tensor
         // (its first and its last row): those are put together element by element
@@ -622,21 +686,15 @@ __device__ __forceinline__ void produce_weights(const Layer& a, const WeightMaps
           bytes = (uint32_t)(to - from);
         }
       }
-      const uint32_t total = __reduce_add_sync(kAll, bytes);
-      if (lane == 0) tma::mbar_arrive_expect_tx(full, total);
+      uint32_t total = (SECOND ? min(16, a.hidden - tile * 16) : 2 * min(8, a.inter - tile * 8)) *
+                       len * 2;
+      if (T == kAny) total = __reduce_add_sync(kAll, bytes);
+      if (lane == 0 && !hold) tma::mbar_arrive_expect_tx(full, total);
       __syncwarp();
       if (bytes > 0) tma::bulk_load(dst, src, bytes, full);
     }
     slot.next(ring);
   });
-}
-
-// Waits until every stage filled has landed: a CTA does not end before its copies.
-__device__ __forceinline__ void drain(const Ring& ring, const Slot& slot, const GiveUp& g) {
-  for (int i = 0; i < ring.stages - slot.fresh; ++i) {
-    const uint32_t parity = i < slot.at ? slot.parity : slot.parity ^ 1u;
-    if (!tma::mbar_wait(&ring.full[i], parity)) flag_error(g.err, MOE_DEVERR_TIMEOUT);
-  }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -647,21 +705,23 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tma::smem_addr(bar))
                : "memory");
 }
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
 
 // The stages' columns of the unit's tokens (second product: of both halves of
 // their activations).  Both lie in rows that end with zeros up to a multiple of 8.
-template <Tiling T, bool SECOND>
+template <Tiling T, bool SECOND, bool STALLED>
 __device__ __forceinline__ void produce_tokens(const Layer& a, const Tables& tb, const Ring& ring,
                                                Slot& slot, const GiveUp& g, int warp, int lane) {
   using S = Tile<T>;
+  int fills = 0;
   for_stages<T>(tb, make_product<T, SECOND>(a, tb), [&](Unit u, int, int k0, int len) {
-    slot.claim(ring, g);
     const uint32_t dst = tma::smem_addr(ring.base + (size_t)slot.at * ring.stage_bytes) +
                          S::kWeightBytes;
     const int rows = SECOND ? 2 * u.count : u.count, pieces = (len + 7) / 8;
+    slot.claim<kTokens>(ring, g, lane);
+    if (STALLED && fills++ == 2 && warp == 0 && withheld<STALLED>(a, kStallTokens)) {
+      slot.next(ring);
+      return;
+    }
     for (int r = warp; r < rows; r += kTokenWarps) {
       const uint16_t* src;
       if (SECOND) {
@@ -868,7 +928,7 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
     for (int c = 0; c < p.chunks; ++c) {
       const int len = min(S::kCols, p.axis - c * S::kCols);
       const uint32_t stage = ring_base + slot.at * ring.stage_bytes;
-      wait_phase(&ring.full[slot.at], slot.parity, g);
+      slot.wait(ring, g);
       __syncwarp();
       WeightAddr<T> w[M];
 #pragma unroll
@@ -886,7 +946,7 @@ __device__ __forceinline__ void consume(const Layer& a, const Tables& tb, const 
       else
         multiply_stage<D, T, SECOND, NT>(acc, w, tokens, boff, lo_off, len, warp, lane);
       __syncwarp();
-      if (lane == 0) tma::mbar_arrive(&ring.empty[slot.at]);
+      if (lane == 0 && !slot.dead()) tma::mbar_arrive(&ring.empty[slot.at]);
       slot.next(ring);
     }
     // The warps' sums, in one tree, a group of tokens at a time; half of the warps finish a
@@ -974,17 +1034,18 @@ __device__ __forceinline__ void combine(const Layer& a, const Tables& tb) {
   }
 }
 
-template <class D, Tiling T>
+template <class D, Tiling T, bool STALLED>
 __global__ void __launch_bounds__(kLayerThreads, 1)
 layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMaps maps) {
   using S = Tile<T>;
   __shared__ Tables tb;
   __shared__ uint64_t bars[2 * kMaxStages];
-  __shared__ int gave_up;
+  __shared__ int gave_up, filled;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     gave_up = 0;
+    filled = -1;
     for (int i = 0; i < kMaxStages; ++i) {
       tma::mbar_init(&bars[i], 1 + kTokenWarps * 32);
       tma::mbar_init(&bars[kMaxStages + i], kConsumers);
@@ -993,41 +1054,43 @@ layer_experts(const __grid_constant__ Layer a, const __grid_constant__ WeightMap
   }
   pdl_prologue();
   // (the ring serves as scratch before its first copies)
-  const GiveUp g{&gave_up, a.err ? a.err : &g_layer_errors};
-  make_tables(a, tb, reinterpret_cast<uint32_t*>(ring_mem), S::kTokens, kLayerThreads, g);
+  const GiveUp g{&gave_up, a.err ? a.err : &g_layer_errors,
+                 STALLED ? a.wait_cycles : tma::kWaitCycles};
+  make_tables<STALLED>(a, tb, reinterpret_cast<uint32_t*>(ring_mem), S::kTokens, kLayerThreads, g);
   fence_async_proxy();                   // ... by bulk copies
   __syncthreads();
   Ring ring;
   ring.base = ring_mem + ((1024u - (tma::smem_addr(ring_mem) & 1023u)) & 1023u);
   ring.full = bars;
   ring.empty = bars + kMaxStages;
+  ring.filled = &filled;
   ring.stage_bytes = (S::kWeightBytes + 2 * tb.most * S::kTokenPitch + 1023) / 1024 * 1024;
   ring.stages = min(kMaxStages, S::kRing / ring.stage_bytes);
   float4* red = reinterpret_cast<float4*>(ring.base + S::kRing);
-  Slot slot(ring);
+  Slot slot;
   if (warp == kConsumers) {
-    produce_weights<T, false>(a, maps, tb, ring, slot, g, lane);
-    produce_weights<T, true>(a, maps, tb, ring, slot, g, lane);
-    if (lane == 0) drain(ring, slot, g);
+    produce_weights<T, false, STALLED>(a, maps, tb, ring, slot, g, lane);
+    produce_weights<T, true, STALLED>(a, maps, tb, ring, slot, g, lane);
+    if (lane == 0) slot.end_weights(ring, g);
     return;
   }
   if (warp > kConsumers) {
     const int w = warp - kConsumers - 1;
-    produce_tokens<T, false>(a, tb, ring, slot, g, w, lane);
+    produce_tokens<T, false, STALLED>(a, tb, ring, slot, g, w, lane);
     if (lane == 0) grid_wait(&a.barrier[1], g);
     __syncwarp();
-    produce_tokens<T, true>(a, tb, ring, slot, g, w, lane);
+    produce_tokens<T, true, STALLED>(a, tb, ring, slot, g, w, lane);
     cp_async_wait();
     return;
   }
   int buffer = 0;
   consume<D, T, false>(a, tb, ring, slot, red, buffer, g);
   consumers_sync();
-  if (threadIdx.x == 0) grid_arrive(&a.barrier[1]);
+  if (threadIdx.x == 0 && !withheld<STALLED>(a, kStallBarrier + 1)) grid_arrive(&a.barrier[1]);
   consume<D, T, true>(a, tb, ring, slot, red, buffer, g);
   consumers_sync();
   if (threadIdx.x == 0) {
-    grid_arrive(&a.barrier[2]);
+    if (!withheld<STALLED>(a, kStallBarrier + 2)) grid_arrive(&a.barrier[2]);
     grid_wait(&a.barrier[2], g);
   }
   consumers_sync();
@@ -1088,10 +1151,10 @@ int weight_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, i
   return r == CUDA_SUCCESS ? MOE_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <class D, Tiling T>
+template <class D, Tiling T, bool STALLED>
 int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t stream) {
   constexpr size_t smem = Tile<T>::kRing + Tile<T>::kReds * Tile<T>::kRed + 1024;
-  if (int rc = ensure_smem_limit((const void*)layer_experts<D, T>, smem)) return rc;
+  if (int rc = ensure_smem_limit((const void*)layer_experts<D, T, STALLED>, smem)) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(kLayerThreads);
@@ -1104,7 +1167,7 @@ int launch_experts(const Layer& a, const WeightMaps& maps, int sms, cudaStream_t
   attr[1].val.programmaticStreamSerializationAllowed = MOE_PDL;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  (void)cudaLaunchKernelEx(&cfg, layer_experts<D, T>, a, maps);
+  (void)cudaLaunchKernelEx(&cfg, layer_experts<D, T, STALLED>, a, maps);
   return check_launch();
 }
 
@@ -1121,7 +1184,7 @@ double tiles_time(const Layer& a, int rows, int sms) {
   return product(2 * (int64_t)a.inter, a.hidden) + product(a.hidden, a.inter);
 }
 
-template <class D>
+template <class D, bool STALLED>
 int launch(const Layer& given, cudaStream_t stream) {
   if (given.router_f32) launch_logits<D, F32>(given, stream);
   else launch_logits<D, D>(given, stream);
@@ -1133,17 +1196,17 @@ int launch(const Layer& given, cudaStream_t stream) {
   if (a.padded_x) {
     a.x = a.padded_x;
     a.ld_x = (a.hidden + 7) / 8 * 8;
-    return launch_experts<D, kAny>(a, maps, sms, stream);
+    return launch_experts<D, kAny, STALLED>(a, maps, sms, stream);
   }
   // The narrow tiles' units hold 8 tokens: more tokens may need the weights again.  One token
   // of eight 4096 x 2048 experts: 75 us in narrow tiles, 78 in wide ones; eight tokens of 64
   // experts of 2048 x 512: 78 and 60.
   if ((a.tokens <= kNarrowTokens && tiles_time(a, 16, sms) <= tiles_time(a, 64, sms)) ||
       a.inter == 0)
-    return launch_experts<D, kNarrow>(a, maps, sms, stream);
+    return launch_experts<D, kNarrow, STALLED>(a, maps, sms, stream);
   if (int rc = weight_map(&maps.w1, a.w1, a.hidden, a.inter, 2 * (int64_t)a.E, 32)) return rc;
   if (int rc = weight_map(&maps.w2, a.w2, a.inter, a.hidden, a.E, 64)) return rc;
-  return launch_experts<D, kWide>(a, maps, sms, stream);
+  return launch_experts<D, kWide, STALLED>(a, maps, sms, stream);
 }
 
 }  // namespace
@@ -1153,6 +1216,8 @@ bool moe_layer_shape_ok(int64_t tokens, int64_t hidden, int64_t inter, int64_t E
          K <= 32 && K <= E && tokens * K <= kMaxSlots && hidden >= 0 && inter >= 0 &&
          hidden <= (1 << 20) && inter <= (1 << 20);
 }
+
+bool moe_layer_stall_ok(int stall) { return stall >= 0 && stall < kStalls; }
 
 int moe_layer_device_errors(int32_t* bits, int clear) {
   cudaError_t e = cudaMemcpyFromSymbol(bits, g_layer_errors, sizeof(int32_t));
@@ -1197,7 +1262,12 @@ int launch_moe_layer(const MoeLayerArgs& m, cudaStream_t stream) {
   a.logits = m.router_w ? a.own_logits : m.logits;
   a.logits_dt = m.router_w ? MOE_FP32 : m.logits_dt;
   a.ld_logits = m.router_w ? m.E : m.ld_logits;
-  return m.dt == MOE_BF16 ? launch<BF16>(a, stream) : launch<F16>(a, stream);
+  if (m.wait_cycles > 0) {
+    a.stall = m.stall;
+    a.wait_cycles = m.wait_cycles;
+    return launch<BF16, true>(a, stream);
+  }
+  return m.dt == MOE_BF16 ? launch<BF16, false>(a, stream) : launch<F16, false>(a, stream);
 }
 
 }  // namespace moe

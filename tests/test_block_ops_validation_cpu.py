@@ -230,3 +230,20 @@ def test_moe_layer_tensors():
     with pytest.raises(_abi.MoeError, match="SHAPE"):
         f(z(129, 64), w1, w2, 2, router_weight=rw)
     _device_error(lambda: f(x, w1, w2, 2, router_weight=rw))
+
+
+def test_moe_layer_stalled_status():
+    n = _abi.moe_layer_small_batch_workspace(4, 64, 32, 8, 2)
+
+    def call(x=FAKE, logits=FAKE, w1=FAKE, w2=FAKE, out=FAKE, ws=FAKE, nbytes=n, tokens=4,
+             hidden=64, inter=32, experts=8, top_k=2, stall=0, cycles=10 ** 5, err=FAKE):
+        return _status(_abi.moe_test_layer_small_batch_stalled, x, logits, w1, w2, out, ws, nbytes,
+                       tokens, hidden, inter, experts, top_k, stall, cycles, err, 0)
+
+    for bad in (dict(stall=-1), dict(stall=6), dict(cycles=999), dict(cycles=2 ** 31 + 1),
+                dict(nbytes=n - 1), dict(tokens=0), dict(tokens=129), dict(hidden=0),
+                dict(inter=0), dict(experts=513), dict(top_k=9)):
+        assert call(**bad) == _abi.MOE_ERR_SHAPE
+    for k in ("x", "logits", "w1", "w2", "out", "ws", "err"):
+        assert call(**{k: None}) == _abi.MOE_ERR_NULL
+        assert call(**{k: FAKE + 1}) == _abi.MOE_ERR_ALIGN

@@ -427,3 +427,38 @@ def test_weights_past_32_bits(cuda_device):
                                      logits=logits[:, [0, e - 1]].contiguous(),
                                      residual=d["residual"])
     assert torch.equal(out, want)
+
+
+# tokens, hidden, inter, experts, top_k of narrow, wide and odd tiles: at least three fills of the
+# first CTA in either product
+STALLS = [("narrow", 2, 4096, 1024, 4, 2), ("wide", 40, 2048, 1024, 8, 4),
+          ("odd", 30, 2047, 515, 8, 4)]
+
+
+@pytest.mark.parametrize("stall", range(6))
+@pytest.mark.parametrize("tiles,tokens,hidden,inter,experts,top_k", STALLS)
+def test_bounded_waits_run_out(cuda_device, tiles, tokens, hidden, inter, experts, top_k, stall):
+    """The first CTA withholds a stage of weights (first or second product), a stage of tokens or
+    an arrival at a grid barrier: the waits give up after 2e7 cycles (10 ms), the producers stop,
+    the copies issued are waited for and the call ends with MOE_DEVERR_TIMEOUT.  The next ordinary
+    calls, on the same workspace, have their bits."""
+    if stall == 3 and tokens <= 24:
+        pytest.skip("every CTA makes the choice for itself")
+    d = _inputs(tokens, hidden, inter, experts, bf, cuda_device, seed=41)
+    g = torch.Generator(device=cuda_device).manual_seed(42)
+    logits = torch.randn(tokens, experts, generator=g, device=cuda_device)
+    ws = torch.empty(ops.moe_layer_small_batch_workspace(tokens, hidden, inter, experts, top_k),
+                     dtype=torch.uint8, device=cuda_device)
+    kw = dict(logits=logits, shared_expert_output=None, residual=None, workspace=ws)
+    want, _, _ = _run(d, top_k, **kw)
+    _abi.moe_device_errors(clear=True)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    out = torch.zeros_like(want)
+    _abi.moe_test_layer_small_batch_stalled(d["x"], logits, d["w1"], d["w2"], out, ws, ws.numel(),
+                                            tokens, hidden, inter, experts, top_k, stall,
+                                            20_000_000, err)
+    torch.cuda.synchronize()
+    assert int(err) == _abi.MOE_DEVERR_TIMEOUT
+    assert _abi.moe_device_errors(clear=True) == 0
+    for _ in range(2):
+        assert torch.equal(_run(d, top_k, **kw)[0], want)
