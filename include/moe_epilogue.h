@@ -606,6 +606,26 @@ MOE_API int moe_test_swiglu_fwd_stalled(const void* x, const float* probs, void*
                                         int32_t* dev_err, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Test hook of the layer norm backward's bounded waits (not for production use).
+ * moe_layer_norm_bwd of contiguous bf16 rows with an fp32 weight and no bias, in
+ * which row stall_row's copies are withheld and every wait gives up after
+ * `wait_cycles` SM cycles.  The team of warps whose row it is fetches nothing more
+ * and waits (as long again at most) for the copies that it asked for;
+ * MOE_DEVERR_TIMEOUT is set in the word of moe_device_errors.  grad_x is void from
+ * that row on in the rows of that team, right in all others; grad_weight is void.
+ * hidden    a multiple of 8 in 513 .. 1024 (16 teams to a CTA) or 4097 .. 8192 (2);
+ *           the teams take rows in turn, of min(148, ceil(rows / teams)) CTAs
+ * stall_row in [0, rows);  wait_cycles  1000 .. 2^31
+ * grad_y, x, weight, grad_x, workspace  16-byte aligned
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_test_layer_norm_bwd_stalled(const void* grad_y, const void* x,
+                                            const float* weight, const float* mean,
+                                            const float* rstd, void* grad_x, float* grad_weight,
+                                            void* workspace, int64_t workspace_bytes,
+                                            int64_t rows, int64_t hidden, int64_t stall_row,
+                                            int64_t wait_cycles, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Test hook of the few-token layer's bounded waits (not for production use).
  * moe_layer_small_batch of contiguous bf16 tensors and fp32 logits (softmax over
  * the chosen experts, no limit, no shared expert, no residual), in which the

@@ -56,6 +56,8 @@ SIGNATURES = {
     "moe_layer_small_batch": [_P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
                               _I64, _I64, _I64, _I32, _I32, _I64, _I64, _I64, _I64, _I64, _I, _I,
                               _F, _F, _P, _P],
+    "moe_test_layer_norm_bwd_stalled": [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64,
+                                        _I64, _P],
     "moe_test_layer_small_batch_stalled": [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32,
                                            _I32, _I32, _I64, _P, _P],
     "moe_symm_alloc": [ctypes.c_size_t, ctypes.POINTER(_P)],
@@ -305,6 +307,15 @@ def moe_layer_small_batch(x, dt, router_weight, router_dt, logits, logits_dt, w1
           tokens, hidden, inter, num_experts, top_k, ld_x, ld_logits, ld_shared, ld_residual,
           ld_out, score, int(bool(normalise)), float(scale), float(limit), ptr(dev_err),
           stream_handle(stream))
+
+
+def moe_test_layer_norm_bwd_stalled(grad_y, x, weight, mean, rstd, grad_x, grad_weight, workspace,
+                                    workspace_bytes, rows, hidden, stall_row, wait_cycles,
+                                    stream=None):
+    """The layer norm's backward with one row's copies withheld (tests)."""
+    _call("moe_test_layer_norm_bwd_stalled", ptr(grad_y), ptr(x), ptr(weight), ptr(mean),
+          ptr(rstd), ptr(grad_x), ptr(grad_weight), ptr(workspace), workspace_bytes, rows, hidden,
+          stall_row, wait_cycles, stream_handle(stream))
 
 
 def moe_test_layer_small_batch_stalled(x, logits, w1, w2, out, workspace, workspace_bytes, tokens,

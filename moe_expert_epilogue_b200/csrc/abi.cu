@@ -488,6 +488,28 @@ int moe_layer_norm_bwd(const void* grad_y, const void* x, const void* weight, co
                                dt, w_dt, stream);
 }
 
+int moe_test_layer_norm_bwd_stalled(const void* grad_y, const void* x, const float* weight,
+                                    const float* mean, const float* rstd, void* grad_x,
+                                    float* grad_weight, void* workspace, int64_t workspace_bytes,
+                                    int64_t rows, int64_t hidden, int64_t stall_row,
+                                    int64_t wait_cycles, cudaStream_t stream) {
+  const bool shape = hidden % kVec == 0 &&
+                     ((hidden > 512 && hidden <= 1024) || (hidden > 4096 && hidden <= 8192));
+  if (!shape || rows < 1 || !product_ok(rows, hidden) || stall_row < 0 || stall_row >= rows ||
+      wait_cycles < 1000 || wait_cycles > tma::kWaitCycles)
+    return MOE_ERR_SHAPE;
+  if (!grad_y || !x || !weight || !mean || !rstd || !grad_x || !grad_weight || !workspace)
+    return MOE_ERR_NULL;
+  if (workspace_bytes < layer_norm_bwd_workspace(rows, hidden)) return MOE_ERR_SHAPE;
+  if (!aligned_to(grad_y, 16) || !aligned_to(x, 16) || !aligned_to(weight, 16) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(grad_x, 16) ||
+      !aligned_to(grad_weight, 4) || !aligned_to(workspace, 16))
+    return MOE_ERR_ALIGN;
+  return launch_layer_norm_bwd_stalled(grad_y, x, weight, mean, rstd, grad_x, grad_weight,
+                                       static_cast<float*>(workspace), rows, hidden, stall_row,
+                                       (long long)wait_cycles, stream);
+}
+
 int moe_router_topk_fwd(const void* logits, moe_dtype dt, float* weights, int32_t* ids,
                         const int32_t* valid_tokens, int64_t tokens, int32_t num_experts,
                         int32_t top_k, int64_t ld_logits, moe_score score, int normalise,

@@ -134,6 +134,12 @@ int launch_layer_norm_bwd(const void* gy, const void* x, const void* w, const fl
                           const float* rstd, void* gx, void* gw, void* gb, float* ws,
                           int64_t rows, int64_t hidden, int64_t ld_gy, int64_t ld_x,
                           int64_t ld_gx, moe_dtype dt, moe_dtype w_dt, cudaStream_t stream);
+// The backward of contiguous bf16 rows (fp32 weights) with one row's copies withheld (tests of the
+// bounded waits; arguments validated by the caller).
+int launch_layer_norm_bwd_stalled(const void* gy, const void* x, const float* w,
+                                  const float* mean, const float* rstd, void* gx, float* gw,
+                                  float* ws, int64_t rows, int64_t hidden, int64_t stall,
+                                  long long limit, cudaStream_t stream);
 int launch_router_topk_fwd(const void* logits, moe_dtype dt, float* weights, int32_t* ids,
                            const int32_t* valid, int64_t tokens, int E, int K, int64_t ld,
                            bool softmax, bool normalise, float scale, int32_t* err,

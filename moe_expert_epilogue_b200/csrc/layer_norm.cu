@@ -360,13 +360,16 @@ __device__ __forceinline__ float warp_sum2(float a, float b) {
 
 constexpr int kBwdThreads = 512;
 
-template <class D, class W, int VEC, int C, int WPR>
+// STALLED (tests of the bounded waits): row `stall`'s copies are withheld, and waits
+// give up after `limit` cycles.
+template <class D, class W, int VEC, int C, int WPR, bool STALLED = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restrict__ x,
               const typename W::T* __restrict__ w, const float* __restrict__ mean,
               const float* __restrict__ rstd, typename D::T* __restrict__ gx,
               float* __restrict__ pw, float* __restrict__ pb, int64_t rows, int hidden,
-              int64_t ld_gy, int64_t ld_x, int64_t ld_gx, int stages) {
+              int64_t ld_gy, int64_t ld_x, int64_t ld_gx, int stages, int64_t stall,
+              long long limit) {
   using T = typename D::T;
   using L = Lanes<VEC>;
   using P = typename L::T;
@@ -389,11 +392,14 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   const uint32_t row_bytes = (uint32_t)hidden * sizeof(T);
   uint8_t* ring = smem + (size_t)team * stages * 2 * row_bytes;
   uint64_t* full = bars + team * 8;
-  // After a wait that gave up nobody waits, and nothing more is fetched.
+  // A thread whose wait gave up waits no more; the team's first thread then fetches nothing more
+  // (as long as it waits itself, it refills a stage only when the copies before have landed), and
+  // waits at the end for what it asked for.
   bool dead = false;
+  const long long cycles = STALLED ? limit : tma::kWaitCycles;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (tma::mbar_try(bar, parity) || dead) return;
-    if (!tma::mbar_wait(bar, parity)) {
+    if (!tma::mbar_wait(bar, parity, cycles)) {
       atomicOr(&g_norm_errors, MOE_DEVERR_TIMEOUT);
       dead = true;
     }
@@ -413,9 +419,11 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
     const int64_t r = first + issued * step;
     uint8_t* dst = ring + (size_t)put * 2 * row_bytes;
     stats[team * 8 + put] = make_float2(next_m, next_rs);
-    tma::mbar_arrive_expect_tx(&full[put], 2 * row_bytes);
-    tma::bulk_load(dst, x + r * ld_x, row_bytes, &full[put]);
-    tma::bulk_load(dst + row_bytes, gy + r * ld_gy, row_bytes, &full[put]);
+    if (!STALLED || r != stall) {
+      tma::mbar_arrive_expect_tx(&full[put], 2 * row_bytes);
+      tma::bulk_load(dst, x + r * ld_x, row_bytes, &full[put]);
+      tma::bulk_load(dst + row_bytes, gy + r * ld_gy, row_bytes, &full[put]);
+    }
     load_stats(++issued);
     if (++put == stages) put = 0;
   };
@@ -581,7 +589,7 @@ norm_bwd_rows(const typename D::T* __restrict__ gy, const typename D::T* __restr
   }
   if (kRing && dead && t == 0)            // before the CTA ends, its copies land
     for (int k = issued > stages ? issued - stages : 0; k < issued; ++k)
-      tma::mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1);
+      tma::mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1, cycles);
   pw += (int64_t)blockIdx.x * hidden;
   pb += (int64_t)blockIdx.x * hidden;
   if constexpr (kTeams > 1) __syncthreads();   // every team is done with its ring
@@ -698,7 +706,7 @@ int fwd(const void* x_, const void* w_, const void* b_, void* y_, float* mean, f
 template <class D, class W>
 int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, const float* rstd,
         void* gx_, void* gw_, void* gb_, float* ws, int64_t rows, int64_t hidden, int64_t ld_gy,
-        int64_t ld_x, int64_t ld_gx, cudaStream_t stream) {
+        int64_t ld_x, int64_t ld_gx, int64_t stall, long long limit, cudaStream_t stream) {
   const auto* gy = static_cast<const typename D::T*>(gy_);
   const auto* x = static_cast<const typename D::T*>(x_);
   const auto* w = static_cast<const typename W::T*>(w_);
@@ -716,14 +724,18 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
     if (teams > 1 && smem < 2 * teams * hidden * 4) smem = 2 * teams * hidden * 4;
     if (int rc = ensure_smem_limit((const void*)k, kBwdSmem)) return rc;
     launch_kernel_block(k, groups, kBwdThreads, (size_t)smem, stream, gy, x, w, mean, rstd, gx, pw,
-                        pb, rows, (int)hidden, ld_gy, ld_x, ld_gx, stages);
+                        pb, rows, (int)hidden, ld_gy, ld_x, ld_gx, stages, stall, limit);
     return check_launch();
   };
   int rc = MOE_OK;
   const bool vec = eights(hidden, {gy, x, w, gx}, {ld_gy, ld_x, ld_gx});
   // 4 units a thread where the ring then holds two stages at least of every team (fp32: 2)
   constexpr int C = D::kBytes == 2 ? 4 : 2, F = 4 / C;
-  if (vec && hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 1>, 8, 16);
+  constexpr bool kStalls = std::is_same<D, BF16>::value && std::is_same<W, F32>::value;
+  if (kStalls && stall >= 0)
+    rc = hidden <= 1024 ? rows_in_registers(norm_bwd_rows<D, W, 8, C, F, kStalls>, 8, 16 / F)
+                        : rows_in_registers(norm_bwd_rows<D, W, 8, C, 8 * F, kStalls>, 8, 2 / F);
+  else if (vec && hidden <= 256) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 1, 1>, 8, 16);
   else if (vec && hidden <= 512) rc = rows_in_registers(norm_bwd_rows<D, W, 8, 2, 1>, 8, 16);
   else if (vec && hidden <= 1024) rc = rows_in_registers(norm_bwd_rows<D, W, 8, C, F>, 8, 16 / F);
   else if (vec && hidden <= 2048)
@@ -792,8 +804,18 @@ int launch_layer_norm_bwd(const void* gy, const void* x, const void* w, const fl
                           const float* rstd, void* gx, void* gw, void* gb, float* ws,
                           int64_t rows, int64_t hidden, int64_t ld_gy, int64_t ld_x,
                           int64_t ld_gx, moe_dtype dt, moe_dtype w_dt, cudaStream_t stream) {
+  const int64_t stall = -1;
+  const long long limit = tma::kWaitCycles;
   MOE_NORM_DISPATCH(bwd, gy, x, w, mean, rstd, gx, gw, gb, ws, rows, hidden, ld_gy, ld_x, ld_gx,
-                    stream)
+                    stall, limit, stream)
+}
+
+int launch_layer_norm_bwd_stalled(const void* gy, const void* x, const float* w,
+                                  const float* mean, const float* rstd, void* gx, float* gw,
+                                  float* ws, int64_t rows, int64_t hidden, int64_t stall,
+                                  long long limit, cudaStream_t stream) {
+  return bwd<BF16, F32>(gy, x, w, mean, rstd, gx, gw, nullptr, ws, rows, hidden, hidden, hidden,
+                        hidden, stall, limit, stream);
 }
 
 }  // namespace moe

@@ -247,3 +247,20 @@ def test_moe_layer_stalled_status():
     for k in ("x", "logits", "w1", "w2", "out", "ws", "err"):
         assert call(**{k: None}) == _abi.MOE_ERR_NULL
         assert call(**{k: FAKE + 1}) == _abi.MOE_ERR_ALIGN
+
+
+def test_layer_norm_bwd_stalled_status():
+    n = _abi.moe_layer_norm_bwd_workspace(40, 1024)
+
+    def call(gy=FAKE, x=FAKE, w=FAKE, mean=FAKE, rstd=FAKE, gx=FAKE, gw=FAKE, ws=FAKE, nbytes=n,
+             rows=40, hidden=1024, stall=3, cycles=10 ** 5):
+        return _status(_abi.moe_test_layer_norm_bwd_stalled, gy, x, w, mean, rstd, gx, gw, ws,
+                       nbytes, rows, hidden, stall, cycles, 0)
+
+    for bad in (dict(hidden=1020), dict(hidden=512), dict(hidden=2048), dict(hidden=8200),
+                dict(rows=0), dict(stall=-1), dict(stall=40), dict(cycles=999),
+                dict(cycles=2 ** 31 + 1), dict(nbytes=n - 1)):
+        assert call(**bad) == _abi.MOE_ERR_SHAPE
+    for k in ("gy", "x", "w", "mean", "rstd", "gx", "gw", "ws"):
+        assert call(**{k: None}) == _abi.MOE_ERR_NULL
+        assert call(**{k: FAKE + 1}) == _abi.MOE_ERR_ALIGN

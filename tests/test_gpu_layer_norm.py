@@ -250,3 +250,32 @@ def test_offsets_past_32_bits(cuda_device):
     out = buf.view(7, ld)[:, 2000:3000]
     ops.layer_norm_bwd(gy, xs, w, mean, rstd, grad_x=out)
     assert torch.equal(out, ops.layer_norm_bwd(gy, x, w, mean, rstd)[0])
+
+
+# rows, hidden, teams of a CTA, the stalled team and its row that is withheld
+@pytest.mark.parametrize("rows,hidden,teams,team,k", [(9000, 1024, 16, 37, 1), (1500, 7168, 2, 5, 3),
+                                                      (1500, 4104, 2, 0, 0)])
+def test_backward_bounded_wait_runs_out(cuda_device, rows, hidden, teams, team, k):
+    """A row whose copies never come: its team gives up after 2e7 cycles (10 ms), the device's
+    error word says so, every other team's rows and that team's rows before are as ever, and so
+    is the next ordinary call."""
+    from moe_expert_epilogue_b200 import _abi
+    x, w, _, gy = _inputs(rows, hidden, bf, f32, 19, cuda_device)
+    _, mean, rstd = ops.layer_norm_fwd(x, w)
+    want = ops.layer_norm_bwd(gy, x, w, mean, rstd, has_bias=False)
+    ws = torch.empty(ops.layer_norm_bwd_workspace(rows, hidden), dtype=torch.uint8,
+                     device=cuda_device)
+    gx, gw = torch.zeros_like(x), torch.zeros_like(w)
+    step = min(148, -(-rows // teams)) * teams
+    stall = team + k * step
+    assert _abi.moe_device_errors(clear=True) == 0
+    _abi.moe_test_layer_norm_bwd_stalled(gy, x, w, mean, rstd, gx, gw, ws, ws.numel(), rows, hidden,
+                                         stall, 20_000_000)
+    torch.cuda.synchronize()
+    assert _abi.moe_device_errors(clear=True) == _abi.MOE_DEVERR_TIMEOUT
+    r = torch.arange(rows, device=cuda_device)
+    whole = (r % step != team) | (r < stall)
+    assert int(whole.sum()) < rows and torch.equal(gx[whole], want[0][whole])
+    again = ops.layer_norm_bwd(gy, x, w, mean, rstd, has_bias=False, workspace=ws)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    assert _abi.moe_device_errors(clear=True) == 0
