@@ -418,3 +418,21 @@ def test_many_tokens_of_extreme_values(cuda_device, dt, experts):
     w = ops.router_topk_fwd(z, 8, SIG, False)[0]
     want = torch.sigmoid(z.double().gather(1, ids.long().clamp(min=0))) * (ids >= 0)
     assert ((w.double() - want).abs() <= 8 * U * want + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("experts", [40, 256, 1000])
+def test_many_fp32_tokens_of_16_bit_values(cuda_device, dt, experts):
+    """fp32 logits that came from a 16-bit type, with many equal ones: the same choice, and the
+    same again with one logit's last bit set, which makes it the larger of its equals."""
+    z, _ = _logits(8300, experts, dt, 51, cuda_device)
+    z[5] = 1.0
+    _, want = ops.router_topk_fwd(z, 8)
+    z32 = z.float()
+    w, ids = ops.router_topk_fwd(z32, 8)
+    assert torch.equal(ids, want) and torch.equal(ids, _sorted_choice(z32, 8))
+    bits = z32.view(torch.int32)
+    up = torch.where(bits >= 0, bits | 1, bits)
+    bits[:, experts - 3] = up[:, experts - 3]
+    _, ids = ops.router_topk_fwd(z32, 8)
+    assert torch.equal(ids, _sorted_choice(z32, 8)) and ids[5, 0] == experts - 3
