@@ -553,7 +553,8 @@ MOE_API int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t*
  * shared_expert_output, residual  dt [tokens, ld_*] or NULL (nothing is added)
  * out             dt [tokens, ld_out]; may equal residual
  * topk_weights    fp32 [tokens, top_k] or NULL: the routing weights (output)
- * topk_ids        int32 [tokens, top_k] or NULL: the chosen experts (output)
+ * topk_ids        int32 [tokens, top_k] or NULL: the chosen experts (output); both
+ *                 are written with hidden == 0 too (without logits, of logits 0)
  * valid_tokens    optional int32 (device): rows of every output at or past it
  *                 stay as they are (MOE_DEVERR_COUNT if outside [0, tokens])
  * workspace       at least moe_layer_small_batch_workspace() bytes, 256-byte

@@ -582,10 +582,15 @@ int moe_layer_small_batch(const void* x, moe_dtype dt, const void* router_weight
       (residual && !product_ok(tokens, ld_residual)))
     return MOE_ERR_SHAPE;
   if (!limit_ok(limit) || !std::isfinite(scale)) return MOE_ERR_LIMIT;
-  if (tokens == 0 || hidden == 0) return MOE_OK;
-  if (!x || !out || !workspace || (router_weight == nullptr) == (logits == nullptr) ||
-      (inter > 0 && (!w1 || !w2)))
+  if (tokens == 0) return MOE_OK;
+  if (hidden == 0) {          // nothing but the choice: of logits 0 where none are given
+    if (!topk_weights && !topk_ids) return MOE_OK;
+    if (!workspace || (router_weight && logits)) return MOE_ERR_NULL;
+    if (!logits) router_weight = workspace;                            // (has no elements)
+  } else if (!x || !out || !workspace || (router_weight == nullptr) == (logits == nullptr) ||
+             (inter > 0 && (!w1 || !w2))) {
     return MOE_ERR_NULL;
+  }
   if (workspace_bytes < moe_layer_workspace(tokens, hidden, inter, num_experts, top_k))
     return MOE_ERR_SHAPE;
   if (!aligned_to(x, 2) || !aligned_to(w1, 2) || !aligned_to(w2, 2) || !aligned_to(out, 2) ||
@@ -599,7 +604,8 @@ int moe_layer_small_batch(const void* x, moe_dtype dt, const void* router_weight
   m.x = x; m.router_w = router_weight; m.logits = logits; m.w1 = w1; m.w2 = w2;
   m.shared = shared_expert_output; m.residual = residual; m.out = out; m.workspace = workspace;
   m.topk_weights = topk_weights; m.topk_ids = topk_ids; m.valid = valid_tokens;
-  m.tokens = (int)tokens; m.hidden = (int)hidden; m.inter = (int)inter;
+  m.tokens = (int)tokens; m.hidden = (int)hidden;
+  m.inter = hidden > 0 ? (int)inter : 0;
   m.E = num_experts; m.K = top_k;
   m.ld_x = ld_x; m.ld_logits = ld_logits; m.ld_shared = ld_shared; m.ld_residual = ld_residual;
   m.ld_out = ld_out;

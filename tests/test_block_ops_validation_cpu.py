@@ -264,3 +264,18 @@ def test_layer_norm_bwd_stalled_status():
     for k in ("gy", "x", "w", "mean", "rstd", "gx", "gw", "ws"):
         assert call(**{k: None}) == _abi.MOE_ERR_NULL
         assert call(**{k: FAKE + 1}) == _abi.MOE_ERR_ALIGN
+
+
+def test_moe_layer_without_columns_status():
+    n = _abi.moe_layer_small_batch_workspace(4, 0, 32, 8, 2)
+
+    def call(rw=None, logits=FAKE, tw=FAKE, ti=FAKE, ws=FAKE, nbytes=n):
+        return (_abi.moe_layer_small_batch, None, BF16, rw, BF16, logits, FP32, None, None, None,
+                None, None, tw, ti, None, ws, nbytes, 4, 0, 32, 8, 2, 0, 8, 0, 0, 0, 0, True, 1.0,
+                7.0, None, 0)
+
+    assert _status(*call(ws=None)) == _status(*call(rw=FAKE)) == _abi.MOE_ERR_NULL
+    assert _status(*call(nbytes=n - 1)) == _abi.MOE_ERR_SHAPE
+    assert _status(*call(logits=FAKE + 2)) == _status(*call(ws=FAKE + 128)) == _abi.MOE_ERR_ALIGN
+    f, *args = call(tw=None, ti=None, ws=None)                # no output at all
+    f(*args)

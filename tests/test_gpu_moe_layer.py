@@ -462,3 +462,20 @@ def test_bounded_waits_run_out(cuda_device, tiles, tokens, hidden, inter, expert
     assert _abi.moe_device_errors(clear=True) == 0
     for _ in range(2):
         assert torch.equal(_run(d, top_k, **kw)[0], want)
+
+
+@pytest.mark.parametrize("inter", [0, 24])
+@pytest.mark.parametrize("tokens", [3, 70])
+def test_the_choice_without_columns(cuda_device, tokens, inter):
+    """A hidden axis of no columns: the choice is made all the same, of the logits given or, with
+    a router of no columns, of logits 0."""
+    e = lambda *shape: torch.empty(*shape, dtype=bf, device=cuda_device)  # noqa: E731
+    d = {"x": e(tokens, 0), "w1": e(9, 2 * inter, 0), "w2": e(9, 0, inter),
+         "router_weight": e(9, 0), "shared_expert_output": e(tokens, 0), "residual": e(tokens, 0)}
+    g = torch.Generator(device=cuda_device).manual_seed(43)
+    logits = torch.randn(tokens, 9, generator=g, device=cuda_device)
+    logits[1] = -INF
+    for z in (logits, None):
+        out, w, ids = _run(d, 4, logits=z)
+        ew, eids = ops.router_topk_fwd(torch.zeros_like(logits) if z is None else z, 4)
+        assert out.shape == (tokens, 0) and torch.equal(ids, eids) and torch.equal(w, ew)
