@@ -479,3 +479,94 @@ def test_the_choice_without_columns(cuda_device, tokens, inter):
         out, w, ids = _run(d, 4, logits=z)
         ew, eids = ops.router_topk_fwd(torch.zeros_like(logits) if z is None else z, 4)
         assert out.shape == (tokens, 0) and torch.equal(ids, eids) and torch.equal(w, ew)
+
+
+# More than 24 live tokens: the CTAs share the choices through the workspace, behind a grid barrier.
+
+
+@pytest.mark.parametrize("tokens", [25, 40, 128])
+@pytest.mark.parametrize("ldt", [f32, bf])
+def test_shared_choices_of_closed_experts(cuda_device, tokens, ldt):
+    """Closed experts, tokens with fewer open ones than choices and with none, over a workspace
+    full of ones."""
+    d = _inputs(tokens, 264, 72, 20, bf, cuda_device, seed=45)
+    g = torch.Generator(device=cuda_device).manual_seed(46)
+    logits = torch.randn(tokens, 20, generator=g, device=cuda_device)
+    logits[torch.rand(tokens, 20, generator=g, device=cuda_device) < 0.5] = -INF
+    logits[3::9] = -INF
+    logits[4] = -INF
+    logits[4, 19] = 1.0
+    logits = logits.to(ldt)
+    ws = torch.full((ops.moe_layer_small_batch_workspace(tokens, 264, 72, 20, 6),), 0xff,
+                    dtype=torch.uint8, device=cuda_device)
+    out, w, ids = _run(d, 6, logits=logits, workspace=ws)
+    ew, eids = _expected_choice(d, 6, logits)
+    assert torch.equal(ids, eids) and torch.equal(w, ew)
+    assert (ids[3] == -1).all() and ids[4].tolist() == [19, -1, -1, -1, -1, -1]
+    _compare(d, out, w, ids, INF)
+    ws.fill_(0xff)
+    out, w, ids = _run(d, 6, logits=torch.full_like(logits, -INF), workspace=ws)
+    assert (ids == -1).all() and (w == 0).all()
+    want = d["residual"].float() + d["shared_expert_output"].float()
+    assert torch.equal(out, want.to(bf))
+
+
+@pytest.mark.parametrize("score", [ops.MOE_SCORE_SOFTMAX, ops.MOE_SCORE_SIGMOID])
+@pytest.mark.parametrize("normalise", [True, False])
+@pytest.mark.parametrize("tokens", [40, 128])
+def test_shared_choices_router_modes(cuda_device, tokens, score, normalise):
+    d = _inputs(tokens, 520, 136, 40, hf, cuda_device, seed=47)
+    kw = dict(score=score, normalise=normalise, scale=1.5)
+    out, w, ids = _run(d, 5, limit=7.0, **kw)
+    ew, eids = _expected_choice(d, 5, **kw)
+    assert torch.equal(ids, eids) and torch.equal(w, ew)
+    _compare(d, out, w, ids, 7.0)
+
+
+@pytest.mark.parametrize("tokens", [40, 128])
+def test_valid_tokens_on_both_sides_of_the_shared_choice(cuda_device, tokens):
+    """One captured graph as the count on the device goes up and down across 24."""
+    d = _inputs(tokens, 264, 72, 6, bf, cuda_device, seed=48)
+    full, w, ids = _run(d, 3)
+    n = torch.tensor([tokens], dtype=torch.int32, device=cuda_device)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    x, out = d["x"].clone(), torch.empty_like(full)
+    w2, ids2 = torch.empty_like(w), torch.empty_like(ids)
+    ws = torch.full((ops.moe_layer_small_batch_workspace(tokens, 264, 72, 6, 3),), 0xff,
+                    dtype=torch.uint8, device=cuda_device)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.moe_layer_small_batch(x, d["w1"], d["w2"], 3, router_weight=d["router_weight"],
+                                  shared_expert_output=d["shared_expert_output"],
+                                  residual=d["residual"], valid_tokens=n, out=out, topk_weights=w2,
+                                  topk_ids=ids2, workspace=ws, dev_err=err)
+    for valid in (tokens, 24, 25, 0, 39, 1, tokens + 1, 23, -3, 26):
+        live = min(max(valid, 0), tokens)
+        x.copy_(d["x"])
+        x[live:] = float("nan")
+        n.fill_(valid)
+        err.zero_()
+        for t, fill in ((out, 5.0), (w2, 7.0), (ids2, 99), (ws, 0xff)):
+            t.fill_(fill)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:live], full[:live]) and (out[live:] == 5).all()
+        assert torch.equal(w2[:live], w[:live]) and (w2[live:] == 7).all()
+        assert torch.equal(ids2[:live], ids[:live]) and (ids2[live:] == 99).all()
+        assert int(err) == (_abi.MOE_DEVERR_COUNT if valid != live else 0)
+
+
+def test_two_streams_at_once_with_shared_choices(cuda_device):
+    """Two calls of different shapes in flight on two streams, three grid barriers each."""
+    d = [_inputs(40, 1024, 512, 16, bf, cuda_device, seed=49),
+         _inputs(64, 768, 256, 8, bf, cuda_device, seed=50)]
+    kw = [dict(router_weight=v["router_weight"], residual=v["residual"]) for v in d]
+    want = [ops.moe_layer_small_batch(v["x"], v["w1"], v["w2"], 4, **k) for v, k in zip(d, kw)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [[ops.moe_layer_small_batch(v["x"], v["w1"], v["w2"], 4, stream=s, **k)
+             for v, k, s in zip(d, kw, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for pair in outs for o, w in zip(pair, want))

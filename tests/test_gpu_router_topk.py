@@ -436,3 +436,30 @@ def test_many_fp32_tokens_of_16_bit_values(cuda_device, dt, experts):
     bits[:, experts - 3] = up[:, experts - 3]
     _, ids = ops.router_topk_fwd(z32, 8)
     assert torch.equal(ids, _sorted_choice(z32, 8)) and ids[5, 0] == experts - 3
+
+
+@pytest.mark.parametrize("score,normalise,scale", MODES)
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("tokens,experts,top_k", [(16390, 40, 9), (20001, 161, 16),
+                                                  (16385, 300, 12), (17001, 64, 17)])
+def test_many_tokens_more_than_eight_choices(cuda_device, tokens, experts, top_k, dt, score,
+                                             normalise, scale):
+    """More than eight choices of more than 16384 tokens, two tokens side by side in a warp where
+    their choices fit one; the last warp's second token is not there."""
+    z, _ = _logits(tokens, experts, dt, tokens, cuda_device, masked=0.3)
+    z[17] = -INF
+    z[tokens - 1, 1:] = -INF
+    w, ids = ops.router_topk_fwd(z, top_k, score, normalise, scale)
+    assert torch.equal(ids, _sorted_choice(z, top_k))
+    want = _weights(z, ids, score, normalise, scale)
+    live = ids >= 0
+    assert ((w.double() - want).abs() <= _tol(experts) * want.abs())[live].all()
+    assert (w[~live] == 0).all()
+    for a, b in ((0, 1), (16, 19), (tokens - 70, tokens)):
+        ws, js = ops.router_topk_fwd(z[a:b], top_k, score, normalise, scale)
+        assert torch.equal(js, ids[a:b]) and torch.equal(ws, w[a:b])
+    valid = torch.tensor([tokens - 2], dtype=torch.int32, device=cuda_device)
+    w2, i2 = torch.full_like(w, 7.0), torch.full_like(ids, 7)
+    ops.router_topk_fwd(z, top_k, score, normalise, scale, weights=w2, ids=i2, valid_tokens=valid)
+    assert torch.equal(i2[:-2], ids[:-2]) and torch.equal(w2[:-2], w[:-2])
+    assert (w2[-2:] == 7).all() and (i2[-2:] == 7).all()
