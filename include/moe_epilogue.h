@@ -536,10 +536,12 @@ MOE_API int moe_router_topk_bwd(const void* logits, moe_dtype dt, const int32_t*
  *   l = x . router_weight^T, or the logits given; ids, p as moe_router_topk_fwd
  *   z = w1[e] . x[t],  h = p * silu(min(z_gate, L)) * clamp(z_up, -L, L)
  *   out[t] = residual[t] + (sum over t's experts, ascending, of w2[e] . h + shared[t])
- * fp32 from the products to the one rounding to dt; h enters the second product
- * as the sum of two dt values (its rounding and what that left), so it keeps
- * 16 bits of mantissa in bf16 and up to 22 in fp16 (in fp16 a finite |h| must stay
- * below 131008).  The router's product is summed in 64 bits and rounded to fp32, so
+ * fp32 from the products to the one rounding to dt; h (with p) enters the second
+ * product as the sum of two dt values (its rounding and what that left): off by at
+ * most 2^-16 |h| in bf16, by max(2^-22 |h|, 2^-25) in fp16, so that an fp16 |h| of
+ * 2^-13 and less has no more than fp16's own digits and below 2^-25 is 0.  An fp16
+ * |h| beyond 131008 becomes infinite; limits up to 256 with p up to 1 keep it below.
+ * The router's product is summed in 64 bits and rounded to fp32, so
  * that no summation order decides between two experts.  A token's result does
  * not depend on the other tokens.  A slot without an expert (id -1) adds nothing.
  * Enqueues two kernels, the second cooperative (one CTA per SM, all resident).

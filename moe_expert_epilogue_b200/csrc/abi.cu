@@ -454,7 +454,7 @@ int moe_layer_norm_fwd(const void* x, const void* weight, const void* bias, void
 
 int moe_layer_norm_bwd_workspace(int64_t rows, int64_t hidden, int64_t* bytes) {
   if (!bytes) return MOE_ERR_NULL;
-  if (rows < 0 || hidden < 0 || !product_ok(2 * 4 * 148, hidden)) return MOE_ERR_SHAPE;
+  if (rows < 0 || !layer_norm_bwd_width_ok(hidden)) return MOE_ERR_SHAPE;
   *bytes = layer_norm_bwd_workspace(rows, hidden);
   return MOE_OK;
 }
@@ -465,9 +465,9 @@ int moe_layer_norm_bwd(const void* grad_y, const void* x, const void* weight, co
                        int64_t ld_gy, int64_t ld_x, int64_t ld_gx, moe_dtype dt, moe_dtype w_dt,
                        cudaStream_t stream) {
   if (!dtype_ok(dt) || (w_dt != dt && w_dt != MOE_FP32)) return MOE_ERR_DTYPE;
-  if (rows < 0 || hidden < 0 || ld_gy < hidden || ld_x < hidden || ld_gx < hidden ||
-      !product_ok(rows, ld_gy) || !product_ok(rows, ld_x) || !product_ok(rows, ld_gx) ||
-      !product_ok(2 * 4 * 148, hidden))
+  if (rows < 0 || !layer_norm_bwd_width_ok(hidden) || ld_gy < hidden || ld_x < hidden ||
+      ld_gx < hidden || !product_ok(rows, ld_gy) || !product_ok(rows, ld_x) ||
+      !product_ok(rows, ld_gx))
     return MOE_ERR_SHAPE;
   if (hidden == 0) return MOE_OK;
   if (!grad_weight) return MOE_ERR_NULL;

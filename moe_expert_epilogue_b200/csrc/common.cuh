@@ -1,9 +1,9 @@
-// common.cuh -- device helpers shared by the epilogue kernels (sm_100a).
+// common.cuh -- device helpers shared by the kernels (sm_100a).
 //
-// Everything on this path is a memory-bound stream: 16-byte vector loads and
-// stores that bypass L1 allocation, fp32 arithmetic in registers, and one
-// rounding to the storage dtype per output element.  Nothing here is a dense
-// contraction, so no tensor-core path exists.
+// Nearly everything is a memory-bound stream: 16-byte vector loads and stores
+// that bypass L1 allocation, fp32 arithmetic in registers, and one rounding to
+// the storage dtype per output element.  The one dense contraction, the experts'
+// products of a few tokens, has its matrix instructions in moe_layer.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -11,7 +11,7 @@
 
 namespace moe {
 
-constexpr int kThreads = 256;  // threads per CTA for every kernel in the library
+constexpr int kThreads = 256;  // threads per CTA, where a kernel does not say otherwise
 constexpr int kVec = 8;        // elements per vector unit ("chunk")
 
 // Storage-type tags.  Each knows how to widen 8 consecutive elements to fp32

@@ -123,7 +123,9 @@ int launch_epilogue_fused(const void* expert_output, const float* row_probs, int
                           moe_dtype dt, int32_t* dev_err, cudaStream_t stream);
 int launch_residual_add(const void* e, const void* s, const void* r, void* out, int64_t numel,
                         moe_dtype dt, cudaStream_t stream);
-// fp32 bytes of the row groups' partial parameter gradients.
+// Whether the bytes below fit 64 bits for any number of rows; fp32 bytes of the row groups'
+// partial parameter gradients.
+bool layer_norm_bwd_width_ok(int64_t hidden);
 int64_t layer_norm_bwd_workspace(int64_t rows, int64_t hidden);
 // Copies (and optionally clears) the layer norm's per-device timeout word.
 int layer_norm_device_errors(int32_t* bits, int clear);

@@ -10,8 +10,8 @@
 // (E[x^2] - mean^2 loses every digit of rows whose mean is large).  The
 // parameter gradients are summed in two fixed steps: up to kNormGroups groups of
 // rows, each in row order, then the groups' partial sums in group order.  The
-// number of groups follows from the sizes alone, so the bits depend neither on
-// the launch nor on the device.
+// groups follow from the sizes, the types and the alignment of the data, so the
+// bits depend neither on the launch nor on the device.
 //
 // HBM bandwidth bounds both passes: the rows are read once, held in registers,
 // and written once.  A warp holds a short row, a CTA a long one; a thread loads
@@ -691,6 +691,10 @@ int fwd(const void* x_, const void* w_, const void* b_, void* y_, float* mean, f
     if (n <= 1024) return rows_in_registers(norm_fwd_rows<D, W, 8, 4, 256>, 1);
     return rows_in_registers(norm_fwd_rows<D, W, 8, 8, 256>, 1);
   }
+  // Single elements, bf16, us: 65536 x 255 with a warp to a row 20.5, with two 29.2; 32768 x 511
+  // with a warp 35.2, with a CTA 45.4; 16384 x 1001 with a CTA 29.7 (fp32 29.8), with four warps
+  // and 8 elements a thread 21.4 (26.1), with two and 16 36.1; 16384 x 2001 with a CTA 42.3, with
+  // four warps 71.7; 8192 x 4001 with a CTA 69.2, with four warps and 32 elements a thread 62.9.
   if (hidden <= 256) return rows_in_registers(norm_fwd_rows<D, W, 1, 8, 32>, 8);
   if (hidden <= 512) return rows_in_registers(norm_fwd_rows<D, W, 1, 16, 32>, 8);
   if (hidden <= 1024) return rows_in_registers(norm_fwd_rows<D, W, 1, 4, 256>, 1);
@@ -769,6 +773,10 @@ int bwd(const void* gy_, const void* x_, const void* w_, const float* mean, cons
 }
 
 }  // namespace
+
+bool layer_norm_bwd_width_ok(int64_t hidden) {
+  return hidden >= 0 && hidden <= INT64_MAX / 8 / (2 * kNormGroups * (int64_t)sizeof(float));
+}
 
 int64_t layer_norm_bwd_workspace(int64_t rows, int64_t hidden) {
   return 2 * (int64_t)norm_groups(rows) * hidden * (int64_t)sizeof(float);

@@ -213,8 +213,8 @@ router_fwd(const typename D::T* __restrict__ logits, float* __restrict__ weights
 // time, sorts them and keeps the eight largest of these and of those it has (the
 // larger of one list's i-th and the other's i-th from the end, then the end of a
 // bitonic sort); two or three such steps between the lanes leave every lane the
-// token's eight.  K <= 8.  A third of the instructions of the rounds above: 32768 x
-// 256, K = 8, bf16 16.6 us there and 10.7 here, fp32 24.2 and 16.8.
+// token's eight.  K <= 8.  About half of the instructions of the rounds above: 32768
+// x 256, K = 8, bf16 16.6 us there and 10.8 here, fp32 24.2 and 18.0.
 // A key is a logit and its expert in one number: pair_key, and of fp32 the upper 22
 // bits of order_key with 0x3ff - expert (E <= 1024).  These order all but logits
 // that agree in 22 bits; so of fp32 the eight are ordered once more by their whole
@@ -568,8 +568,8 @@ int launch_fwd(const void* logits, float* weights, int32_t* ids, const int32_t* 
   // warp, 3.1 with eight lanes to a token; 4096: 4.0 and 3.2; fp32 4096: 5.0 and 5.9, 8192: 8.2 and
   // 7.5).  Four lanes need fewer steps between lanes, eight more of them at once (16384 x 256:
   // 6.6 us both, 32768: 10.7 with four, 11.9 with eight), and the sums over all experts wait less
-  // with fewer tokens a warp (32768: 19.0 and 18.0), as do the second looks of fp32 (18.2 and
-  // 16.8).
+  // with fewer tokens a warp (32768: 19.0 and 18.0), as do the second looks of fp32 (19.0 and
+  // 17.9; of 512 experts 31.9 and 32.4).
   constexpr bool kHalf = D::kBytes == 2;
   if (K <= 8 && tokens >= (kHalf ? 4096 : 8192)) {
     const bool wide =

@@ -495,9 +495,10 @@ def moe_layer_small_batch(x, w1, w2, top_k, router_weight=None, logits=None,
                           limit=float("inf"), shared_expert_output=None, residual=None,
                           valid_tokens=None, out=None, topk_weights=None, topk_ids=None,
                           workspace=None, dev_err=None, stream=None):
-    """A whole mixture-of-experts layer for up to 128 tokens (bf16 or fp16):
+    """A whole mixture-of-experts layer for a few tokens (bf16 or fp16):
     out = residual + (sum over each token's experts of its routing weight times
     w2[e] (clamped SwiGLU of w1[e] x) + shared_expert_output).
+    Up to 128 tokens, tokens * top_k up to 1024, up to 512 experts.
 
     x [tokens, hidden]; w1 [experts, 2*inter, hidden] (gate rows first);
     w2 [experts, hidden, inter]; router_weight [experts, hidden] (x's dtype or fp32)
@@ -505,7 +506,11 @@ def moe_layer_small_batch(x, w1, w2, top_k, router_weight=None, logits=None,
     as swiglu_clamped_fwd.  topk_weights (fp32) and topk_ids (int32), [tokens, top_k],
     receive the choice if given.  Rows at or past valid_tokens (int32 [1] on the
     device) stay as they are.  out may be residual.  workspace (uint8, 256-byte
-    aligned, at least moe_layer_small_batch_workspace bytes) is allocated unless given."""
+    aligned, at least moe_layer_small_batch_workspace bytes) is allocated unless given.
+
+    In fp16 the weighted activation that enters the second product is off by up to
+    max(2^-22 of it, 2^-25), and infinite beyond 131008 (limits up to 256 with routing
+    weights up to 1 keep it below); in bf16 by up to 2^-16 of it."""
     tokens, hidden = _two_d(x, "x")
     _check(x, "x", dtype=(torch.bfloat16, torch.float16), contiguous=False)
     dt = x.dtype
