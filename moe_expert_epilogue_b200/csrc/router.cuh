@@ -45,12 +45,6 @@ __device__ __forceinline__ float exp_sum(const float (&v)[V], float top) {
   return warp_sum(s);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
-
 // The number of live tokens: *valid clamped to [0, tokens].
 __device__ __forceinline__ int64_t live_tokens(const int32_t* valid, int64_t tokens,
                                                int32_t* err) {
