@@ -130,9 +130,9 @@ MOE_API int moe_abi_version(void);
 /* Error bits recorded on the current device by calls that were given no
  * error word of their own (today: the TMA-staged clamped-SwiGLU forward
  * through moe_swiglu_clamped_fwd, or _ex with dev_err NULL, the layer norm's
- * backward, and moe_layer_small_batch with dev_err NULL: MOE_DEVERR_TIMEOUT).  One word per device, shared by every stream and
- * thread; pass dev_err to moe_swiglu_clamped_fwd_ex to keep a call's bits
- * apart.  Synchronous: waits for the device, copies the word into *bits and,
+ * backward, and moe_layer_small_batch with dev_err NULL: MOE_DEVERR_TIMEOUT).
+ * One word per device, shared by every stream and thread; pass dev_err where an
+ * entry point takes one to keep a call's bits apart.  Synchronous: waits for the device, copies the word into *bits and,
  * if `clear`, resets it.  Returns MOE_OK, MOE_ERR_NULL or MOE_ERR_CUDA. */
 MOE_API int moe_device_errors(int32_t* bits, int clear);
 
