@@ -570,3 +570,16 @@ def test_two_streams_at_once_with_shared_choices(cuda_device):
              for v, k, s in zip(d, kw, streams)] for _ in range(10)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for pair in outs for o, w in zip(pair, want))
+
+
+@pytest.mark.parametrize("ldt", [f32, hf])
+@pytest.mark.parametrize("tokens", [7, 50])
+def test_logits_inside_a_wider_buffer(cuda_device, tokens, ldt):
+    d = _inputs(tokens, 136, 40, 21, bf, cuda_device, seed=52)
+    g = torch.Generator(device=cuda_device).manual_seed(53)
+    wide = torch.randn(tokens, 30, generator=g, device=cuda_device).to(ldt) + 9
+    part = wide[:, 5:26]
+    got, want = _run(d, 4, logits=part), _run(d, 4, logits=part.contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ew, eids = _expected_choice(d, 4, part)
+    assert torch.equal(got[2], eids) and torch.equal(got[1], ew)
